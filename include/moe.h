@@ -313,6 +313,87 @@ int moe_forward_paged(const moe_config* cfg, const void* x, const moe_weights* h
                       hipStream_t stream);
 
 /*
+ * Dense operators in 8 bits: what stands around the MoE blocks of a decoder stack (TensorFold
+ * #1247, config paragraph: 24 layers of which layer 0 is dense).  Same conventions as above;
+ * all matrices are row-major and contiguous.  Pointers are 16-byte aligned unless noted.
+ *
+ * moe_norm_quant_rows: one pass over `rows` rows of `width` act_dtype elements,
+ *   s = round(x + residual)   (x itself when residual is NULL), stored to x_sum [rows, width];
+ *   v = s / sqrt(mean over width of s^2 + norm_eps) * norm_weight   (s itself when NULL);
+ *   out, scales by `format`:
+ *     MOE_ROWS_ACT         round(v) [rows, width] act_dtype; no scales;
+ *     MOE_ROWS_I8          int8 codes [rows, width], scales fp32 [rows]:
+ *                          scale = amax / 127, code = rne(v / scale) in [-127, 127];
+ *     MOE_ROWS_E4M3_B128   e4m3 codes, scales fp32 [rows, width/128] = amax of the block / 448;
+ *     MOE_ROWS_MXFP8       e4m3 codes, scales uint8 [rows, width/32], E8M0
+ *                          (floor(log2 amax) - 8, the byte is that + 127).
+ * round() is to act_dtype (round to nearest even); everything else is fp32, and the codes are
+ * taken from the fp32 v.  A row or block whose amax/127 (amax/448) is below the smallest
+ * normal fp32 has scale 1 (code 0 of E8M0 for a zero MXFP8 block).  With norm_weight and
+ * residual NULL the call quantises (MOE_ROWS_I8 over [out, in] weights gives the codes and
+ * channel scales the products below take).
+ * act_dtype MOE_F32 or MOE_BF16; width a multiple of 8 (128 for E4M3_B128, 32 for MXFP8), at
+ * most 32768; rows < 2^31.  x_sum (required with a residual, else ignored) may be x or
+ * residual, and a MOE_ROWS_ACT out may be x or residual; other overlaps are not allowed.
+ * Scales need their own type's alignment only.
+ */
+#define MOE_ROWS_ACT        0
+#define MOE_ROWS_I8         1
+#define MOE_ROWS_E4M3_B128  2
+#define MOE_ROWS_MXFP8      3
+int moe_norm_quant_rows(int64_t rows, int32_t width, int32_t act_dtype, int32_t format,
+                        const void* x, const void* residual, const void* norm_weight,
+                        float norm_eps, void* x_sum, void* out, void* scales, hipStream_t stream);
+
+/*
+ * Product of 8-bit rows and 8-bit weights, a scale per token and per output channel:
+ *   y[t,n] = round(x_scales[t] * w_scales[n] * sum_k x[t,k] w[n,k]  (+ residual[t,n])).
+ * x [rows, in_width], w [out_width, in_width] int8 (any codes, -128 included); scales fp32,
+ * y and residual [rows, out_width] out_dtype (MOE_F32 or MOE_BF16), aligned to their type;
+ * residual may be NULL or y itself.  The sum is exact (int32), so results do not depend on
+ * the batch a row comes in.  in_width a multiple of 16, at most 65536; rows < 2^31.
+ */
+int moe_linear_i8(int64_t rows, int32_t in_width, int32_t out_width, int32_t out_dtype,
+                  const int8_t* x, const float* x_scales, const int8_t* w, const float* w_scales,
+                  const void* residual, void* y, hipStream_t stream);
+
+/*
+ * The gated pair of such products and its activation in one kernel:
+ *   h[t,n] = round(silu(g) * u),  g = x_scales[t] s_gate[n] sum_k x[t,k] w_gate[n,k],  u likewise.
+ * Arguments and limits as moe_linear_i8.
+ */
+int moe_glu_i8(int64_t rows, int32_t in_width, int32_t out_width, int32_t out_dtype,
+               const int8_t* x, const float* x_scales, const int8_t* w_gate, const float* s_gate,
+               const int8_t* w_up, const float* s_up, void* h, hipStream_t stream);
+
+/*
+ * A dense decoder layer's feed-forward block in 8 bits, the sibling of moe_forward_residual:
+ *   x_out = round(x + down(i8(round(glu(i8(RMSNorm(x) * norm_weight))))))
+ * with i8() the per-token quantisation of moe_norm_quant_rows and h rounded to act_dtype
+ * between the products.  x, x_out [T, H] act_dtype; x_out may be x itself.  hidden and
+ * intermediate are multiples of 16, at most 32768.  ws: moe_dense_workspace_size() bytes,
+ * 256-byte aligned.
+ */
+typedef struct {
+  int64_t num_tokens;     /* T */
+  int32_t hidden;         /* H */
+  int32_t intermediate;   /* I */
+  int32_t act_dtype;      /* x, norm weight, x_out: MOE_F32 | MOE_BF16 */
+} moe_dense_config;
+typedef struct {
+  const int8_t* w_gate;   /* [I, H] codes */
+  const int8_t* w_up;     /* [I, H] */
+  const int8_t* w_down;   /* [H, I] */
+  const float*  s_gate;   /* [I] channel scales */
+  const float*  s_up;     /* [I] */
+  const float*  s_down;   /* [H] */
+} moe_dense_weights;
+int moe_dense_workspace_size(const moe_dense_config* cfg, size_t* bytes);
+int moe_dense_residual_i8(const moe_dense_config* cfg, const void* x, const void* norm_weight,
+                          float norm_eps, const moe_dense_weights* w, void* x_out, void* ws,
+                          size_t ws_bytes, hipStream_t stream);
+
+/*
  * Where a call leaves inspectable intermediate results in the workspace, for tests
  * and debugging (host only, no device work).  After moe_forward / moe_forward_timed /
  * moe_forward_residual (and moe_route with logits == NULL) the workspace holds:

@@ -38,10 +38,23 @@ class MoeWeights(ctypes.Structure):
         "sh_b_gate", "sh_b_up", "sh_b_down", "sh_g_gate", "sh_g_up", "sh_g_down")]
 
 
+class DenseConfig(ctypes.Structure):
+    _fields_ = [("num_tokens", ctypes.c_int64), ("hidden", ctypes.c_int32),
+                ("intermediate", ctypes.c_int32), ("act_dtype", ctypes.c_int32)]
+
+
+class DenseWeights(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("w_gate", "w_up", "w_down", "s_gate", "s_up",
+                                               "s_down")]
+
+
 ENTRY_POINTS = ("moe_workspace_size", "moe_route", "moe_permute", "moe_expert_ffn",
                 "moe_combine", "moe_forward", "moe_forward_timed", "moe_forward_residual",
                 "moe_workspace_slot", "moe_forward_noalloc", "moe_pager_state_layout",
-                "moe_pager_reset", "moe_paged_workspace_size", "moe_forward_paged", "moe_strerror")
+                "moe_pager_reset", "moe_paged_workspace_size", "moe_forward_paged",
+                "moe_norm_quant_rows", "moe_linear_i8", "moe_glu_i8", "moe_dense_workspace_size",
+                "moe_dense_residual_i8", "moe_strerror")
+ROW_FORMATS = {"rows": 0, "i8": 1, "e4m3": 2, "mxfp8": 3}   # MOE_ROWS_*
 NOALLOC_SCRATCH_BYTES = 16 << 20   # MOE_NOALLOC_SCRATCH_BYTES
 WS_LOGITS, WS_ACT_CODES, WS_ACT_SCALES, WS_NORM_ROWS = 0, 1, 2, 3   # MOE_WS_* slots
 TIMED_EVENTS = 4   # MOE_TIMED_EVENTS: start/stop of the gate/up kernel, start/stop of the down kernel
@@ -61,6 +74,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     P, SZ = ctypes.c_void_p, ctypes.c_size_t
     cfgp = ctypes.POINTER(MoeConfig)
     wp = ctypes.POINTER(MoeWeights)
+    I32, I64 = ctypes.c_int32, ctypes.c_int64
+    dcfgp, dwp = ctypes.POINTER(DenseConfig), ctypes.POINTER(DenseWeights)
     sig = {
         "moe_workspace_size": [cfgp, ctypes.POINTER(SZ)],
         "moe_route": [cfgp, P, P, P, P, P, P, P, SZ, P],
@@ -76,6 +91,11 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "moe_pager_reset": [cfgp, ctypes.c_int32, P, P],
         "moe_paged_workspace_size": [cfgp, ctypes.c_int32, ctypes.POINTER(SZ)],
         "moe_forward_paged": [cfgp, P, wp, wp, ctypes.c_int32, P, P, P, P, P, SZ, P],
+        "moe_norm_quant_rows": [I64, I32, I32, I32, P, P, P, ctypes.c_float, P, P, P, P],
+        "moe_linear_i8": [I64, I32, I32, I32, P, P, P, P, P, P, P],
+        "moe_glu_i8": [I64, I32, I32, I32, P, P, P, P, P, P, P, P],
+        "moe_dense_workspace_size": [dcfgp, ctypes.POINTER(SZ)],
+        "moe_dense_residual_i8": [dcfgp, P, P, ctypes.c_float, dwp, P, P, SZ, P],
     }
     for name, args in sig.items():
         fn = getattr(lib, name)
@@ -294,3 +314,154 @@ def forward_timed(cfg, x, wst: MoeWeights, ws, y, events_array) -> None:
     _check(load_library().moe_forward_timed(ctypes.byref(cfg), _ptr(x), ctypes.byref(wst), _ptr(y),
                                             None, None, _ptr(ws), ws.numel(), _stream(),
                                             events_array))
+
+
+# ------------------------------------------------------------- dense operators in 8 bits
+
+_ACT = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
+
+
+def _arg(name: str, t: torch.Tensor, shape: tuple, dtype: torch.dtype) -> int:
+    """Device pointer of a contiguous tensor of exactly this shape and type on the current
+    device (the library launches on that device and checks nothing behind a pointer)."""
+    if t.dtype != dtype or tuple(t.shape) != shape:
+        raise ValueError(f"{name}: expected {dtype} {shape}, got {t.dtype} {tuple(t.shape)}")
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name}: expected a tensor on the current device, got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: contiguous tensors only")
+    return t.data_ptr()
+
+
+def _act_dtype(name: str, dtype: torch.dtype) -> int:
+    if dtype not in _ACT:
+        raise ValueError(f"{name}: float32 or bfloat16 only, got {dtype}")
+    return _ACT[dtype]
+
+
+def _rows_of(name: str, t: torch.Tensor):
+    if t.dim() != 2:
+        raise ValueError(f"{name}: expected [rows, width], got {tuple(t.shape)}")
+    return t.shape
+
+
+def norm_quant_rows(x, fmt: str, norm_weight: Optional[torch.Tensor] = None,
+                    residual: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                    x_sum: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                    scales: Optional[torch.Tensor] = None):
+    """Residual add, RMSNorm and output format of rows in one kernel (moe_norm_quant_rows).
+    `fmt`: "rows" (x's type), "i8" (int8 codes, fp32 scale per row), "e4m3" (uint8 codes, fp32
+    scale per 128 columns) or "mxfp8" (uint8 codes, uint8 E8M0 scale per 32).  Without
+    norm_weight the (summed) rows themselves are converted.  x_sum may be x or residual, a
+    "rows" out too.  Returns (out, scales or None, x_sum or None)."""
+    T, H = _rows_of("x", x)
+    act = _act_dtype("x", x.dtype)
+    if fmt not in ROW_FORMATS:
+        raise ValueError(f"fmt: one of {tuple(ROW_FORMATS)}, got {fmt!r}")
+    xp = _arg("x", x, (T, H), x.dtype)
+    rp = sp = cp = gp = None
+    if norm_weight is not None:
+        gp = _arg("norm_weight", norm_weight, (H,), x.dtype)
+    if residual is not None:
+        rp = _arg("residual", residual, (T, H), x.dtype)
+        if x_sum is None:
+            x_sum = torch.empty_like(x)
+        sp = _arg("x_sum", x_sum, (T, H), x.dtype)
+    else:
+        x_sum = None
+    odt = x.dtype if fmt == "rows" else torch.int8 if fmt == "i8" else torch.uint8
+    if out is None:
+        out = torch.empty((T, H), dtype=odt, device=x.device)
+    op = _arg("out", out, (T, H), odt)
+    if fmt == "rows":
+        scales = None
+    else:
+        shape = (T,) if fmt == "i8" else (T, H // 128) if fmt == "e4m3" else (T, H // 32)
+        sdt = torch.uint8 if fmt == "mxfp8" else torch.float32
+        if scales is None:
+            scales = torch.empty(shape, dtype=sdt, device=x.device)
+        cp = _arg("scales", scales, shape, sdt)
+    _check(load_library().moe_norm_quant_rows(T, H, act, ROW_FORMATS[fmt], xp, rp, gp, eps, sp, op,
+                                              cp, _stream()))
+    return out, scales, x_sum
+
+
+def linear_i8(x_codes, x_scales, w_codes, w_scales, out_dtype=torch.bfloat16,
+              residual: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None):
+    """y = (x_codes @ w_codes.T) * x_scales[:, None] * w_scales (+ residual): int8 [T, K] and
+    [N, K] codes, fp32 scales per token and per channel, y [T, N] bf16 or fp32
+    (moe_linear_i8).  residual may be y itself."""
+    T, K = _rows_of("x_codes", x_codes)
+    N = _rows_of("w_codes", w_codes)[0]
+    out = _act_dtype("out_dtype", out_dtype)
+    xp = _arg("x_codes", x_codes, (T, K), torch.int8)
+    sp = _arg("x_scales", x_scales, (T,), torch.float32)
+    wp = _arg("w_codes", w_codes, (N, K), torch.int8)
+    cp = _arg("w_scales", w_scales, (N,), torch.float32)
+    rp = None if residual is None else _arg("residual", residual, (T, N), out_dtype)
+    if y is None:
+        y = torch.empty((T, N), dtype=out_dtype, device=x_codes.device)
+    yp = _arg("y", y, (T, N), out_dtype)
+    _check(load_library().moe_linear_i8(T, K, N, out, xp, sp, wp, cp, rp, yp, _stream()))
+    return y
+
+
+def glu_i8(x_codes, x_scales, w_gate, s_gate, w_up, s_up, out_dtype=torch.bfloat16,
+           h: Optional[torch.Tensor] = None):
+    """h = silu(g) * u with g and u the two 8-bit products of linear_i8, in one kernel
+    (moe_glu_i8).  Returns h [T, N] bf16 or fp32."""
+    T, K = _rows_of("x_codes", x_codes)
+    N = _rows_of("w_gate", w_gate)[0]
+    out = _act_dtype("out_dtype", out_dtype)
+    xp = _arg("x_codes", x_codes, (T, K), torch.int8)
+    sp = _arg("x_scales", x_scales, (T,), torch.float32)
+    gp = _arg("w_gate", w_gate, (N, K), torch.int8)
+    gs = _arg("s_gate", s_gate, (N,), torch.float32)
+    up = _arg("w_up", w_up, (N, K), torch.int8)
+    us = _arg("s_up", s_up, (N,), torch.float32)
+    if h is None:
+        h = torch.empty((T, N), dtype=out_dtype, device=x_codes.device)
+    hp = _arg("h", h, (T, N), out_dtype)
+    _check(load_library().moe_glu_i8(T, K, N, out, xp, sp, gp, gs, up, us, hp, _stream()))
+    return h
+
+
+def make_dense_config(T: int, H: int, I: int, act: str = "bf16") -> DenseConfig:
+    return DenseConfig(T, H, I, _DTYPES[act])
+
+
+def dense_workspace_size(cfg: DenseConfig) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load_library().moe_dense_workspace_size(ctypes.byref(cfg), ctypes.byref(n)))
+    return int(n.value)
+
+
+def alloc_dense_workspace(cfg: DenseConfig, device="cuda") -> torch.Tensor:
+    return torch.empty(max(dense_workspace_size(cfg), 256), dtype=torch.uint8, device=device)
+
+
+def dense_weights_struct(w: dict) -> DenseWeights:
+    """Weight struct of a dict of CUDA tensors: w_gate, w_up [I, H] and w_down [H, I] int8,
+    s_gate, s_up [I] and s_down [H] fp32.  It holds pointers only: keep the tensors alive."""
+    I, H = _rows_of("w_gate", w["w_gate"])
+    shapes = {"w_gate": (I, H), "w_up": (I, H), "w_down": (H, I), "s_gate": (I,), "s_up": (I,),
+              "s_down": (H,)}
+    return DenseWeights(*[_arg(n, w[n], shapes[n], torch.int8 if n[0] == "w" else torch.float32)
+                          for n, _ in DenseWeights._fields_])
+
+
+def dense_residual_i8(cfg: DenseConfig, x, norm_weight, wst: DenseWeights, ws,
+                      x_out: Optional[torch.Tensor] = None, eps: float = 1e-6):
+    """A dense decoder layer's feed-forward block in 8 bits: x_out = x + down(i8(glu(i8(
+    RMSNorm(x) * norm_weight)))) (moe_dense_residual_i8).  x_out may be x itself."""
+    T, H = cfg.num_tokens, cfg.hidden
+    dtype = torch.float32 if cfg.act_dtype == MOE_F32 else torch.bfloat16
+    xp = _arg("x", x, (T, H), dtype)
+    gp = _arg("norm_weight", norm_weight, (H,), dtype)
+    if x_out is None:
+        x_out = torch.empty_like(x)
+    op = _arg("x_out", x_out, (T, H), dtype)
+    wp = _arg("ws", ws, (ws.numel(),), torch.uint8)
+    _check(load_library().moe_dense_residual_i8(ctypes.byref(cfg), xp, gp, eps, ctypes.byref(wst),
+                                                op, wp, ws.numel(), _stream()))
+    return x_out

@@ -15,7 +15,7 @@ LIB = os.path.join(PKG, "libmoe.so")
 
 SOURCES = ["moe_api.hip", "route.hip", "permute.hip", "ffn_skinny.hip", "ffn_mfma.hip",
            "combine.hip", "decode.hip", "pager.hip",
-           "ffn_mx.hip"]
+           "ffn_mx.hip", "norm_quant.hip", "linear_i8.hip", "dense_api.hip"]
 ARCH = "gfx950"
 FLAGS = [
     "-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",

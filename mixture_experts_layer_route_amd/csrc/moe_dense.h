@@ -1,0 +1,85 @@
+// Internals of the dense 8-bit operators: row norm + quantisation, 8-bit products.
+#pragma once
+
+#include <algorithm>
+
+#include "moe_internal.h"
+
+namespace moe {
+
+constexpr int kNormMaxWidth = 32768;    // widest row: 1024 threads x 4 chunks of 8
+constexpr int kI8MaxWidth = 65536;      // |sum| <= 65536 * 128 * 128 = 2^30: int32 sums are exact
+
+struct NormQuant {
+  int64_t rows;
+  int width, act, format;
+  const void* x;
+  const void* res;     // null: no residual
+  const void* gamma;   // null: no norm
+  float eps;
+  void* x_sum;
+  void* out;
+  void* scales;
+};
+int launch_norm_quant(const NormQuant& q, hipStream_t st);
+
+// y = act(x w^T * scales): one weight matrix, or gate and up for the gated product
+struct I8Product {
+  int64_t T;
+  int K, N;
+  int out;                 // MOE_F32 | MOE_BF16
+  const int8_t* x;         // [T, K]
+  const float* sx;         // [T]
+  const int8_t* w;         // [N, K]
+  const float* sw;         // [N]
+  const int8_t* w_up;      // gated product: the up matrix, else null
+  const float* s_up;
+  const void* res;         // [T, N] out type, or null
+  void* y;                 // [T, N] out type
+};
+int launch_i8_product(const I8Product& p, hipStream_t st);
+
+#ifdef __HIPCC__
+// Per-row int8: scale = amax / 127.  A row whose amax is so small that the scale would leave
+// the normal floats (or is zero) has scale 1 and codes 0, so no division overflows.
+__device__ __forceinline__ float i8_scale(float amax) {
+  const float s = amax / 127.0f;
+  return s >= 1.17549435e-38f ? s : 1.0f;
+}
+// the block-FP8 rule of quant_e4m3_wave with the same guard
+__device__ __forceinline__ float e4m3_scale(float amax) {
+  const float s = amax / 448.0f;
+  return s >= 1.17549435e-38f ? s : 1.0f;
+}
+// Eight values -> eight int8 codes, round to nearest even (|v| / scale <= 127 up to the
+// division's rounding, which the clamp takes back).
+__device__ __forceinline__ uint2 i8x8(const float (&v)[8], float scale) {
+  uint32_t w[2] = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float q = fminf(fmaxf(rintf(v[i] / scale), -127.f), 127.f);
+    w[i / 4] |= (uint32_t(int(q)) & 0xFFu) << (8 * (i % 4));
+  }
+  return make_uint2(w[0], w[1]);
+}
+__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ void store8(bf16_t* p, const float (&v)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    w[i] = uint32_t(f32_to_bf16(v[2 * i])) | (uint32_t(f32_to_bf16(v[2 * i + 1])) << 16);
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+// p = round(a + b); a is replaced by the rounded sum
+template <typename TA>
+__device__ __forceinline__ void add_store8(TA* p, float (&a)[8], const float (&b)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) a[i] = to_f32<TA>(from_f32<TA>(a[i] + b[i]));
+  store8(p, a);
+}
+#endif
+
+}  // namespace moe
