@@ -351,7 +351,8 @@ int moe_norm_quant_rows(int64_t rows, int32_t width, int32_t act_dtype, int32_t 
  * x [rows, in_width], w [out_width, in_width] int8 (any codes, -128 included); scales fp32,
  * y and residual [rows, out_width] out_dtype (MOE_F32 or MOE_BF16), aligned to their type;
  * residual may be NULL or y itself.  The sum is exact (int32), so results do not depend on
- * the batch a row comes in.  in_width a multiple of 16, at most 65536; rows < 2^31.
+ * the batch a row comes in.  in_width a multiple of 16, at most 65536; rows < 2^31,
+ * out_width <= 2^30, rows * out_width <= 2^40.
  */
 int moe_linear_i8(int64_t rows, int32_t in_width, int32_t out_width, int32_t out_dtype,
                   const int8_t* x, const float* x_scales, const int8_t* w, const float* w_scales,
@@ -368,8 +369,8 @@ int moe_glu_i8(int64_t rows, int32_t in_width, int32_t out_width, int32_t out_dt
 
 /*
  * A dense decoder layer's feed-forward block in 8 bits, the sibling of moe_forward_residual:
- *   x_out = round(x + down(i8(round(glu(i8(RMSNorm(x) * norm_weight))))))
- * with i8() the per-token quantisation of moe_norm_quant_rows and h rounded to act_dtype
+ *   x_out = round(x + down(i8(glu(i8(RMSNorm(x) * norm_weight)))))
+ * with i8() the per-token quantisation of moe_norm_quant_rows; h is not rounded to act_dtype
  * between the products.  x, x_out [T, H] act_dtype; x_out may be x itself.  hidden and
  * intermediate are multiples of 16, at most 32768.  ws: moe_dense_workspace_size() bytes,
  * 256-byte aligned.

@@ -40,7 +40,8 @@ static int check_product(const I8Product& p, bool glu) {
   if ((reinterpret_cast<uintptr_t>(p.y) | reinterpret_cast<uintptr_t>(p.res)) & natural)
     return MOE_ERR_ARG;
   if (p.K % 16 || p.K > kI8MaxWidth) return MOE_ERR_UNSUPPORTED;
-  if (p.T >= (int64_t(1) << 31) || p.N > (1 << 30)) return MOE_ERR_UNSUPPORTED;
+  if (p.T >= (int64_t(1) << 31) || p.N > (1 << 30) || p.T > (int64_t(1) << 40) / p.N)
+    return MOE_ERR_UNSUPPORTED;   // (2^40 outputs: tile counts stay in 32 bits)
   return MOE_OK;
 }
 
@@ -67,7 +68,7 @@ static int make_dense_plan(const moe_dense_config* c, DensePlan* out) {
   auto take = [&](size_t bytes) { const size_t at = o; o = align256(o + bytes); return at; };
   q.o_xq = take(size_t(q.T) * q.H);
   q.o_sx = take(size_t(q.T) * 4);
-  q.o_h = take(size_t(q.T) * q.I * act_bytes(q.act));
+  q.o_h = take(size_t(q.T) * q.I * 4);   // fp32: h is rounded once, to its codes
   q.o_hq = take(size_t(q.T) * q.I);
   q.o_sh = take(size_t(q.T) * 4);
   q.total = o;
@@ -128,8 +129,8 @@ int moe_dense_residual_i8(const moe_dense_config* cfg, const void* x, const void
   int8_t* hq = reinterpret_cast<int8_t*>(base + q.o_hq);
   float* sh = reinterpret_cast<float*>(base + q.o_sh);
   const NormQuant nx{q.T, q.H, q.act, MOE_ROWS_I8, x, nullptr, norm_weight, norm_eps, nullptr, xq, sx};
-  const I8Product up{q.T, q.H, q.I, q.act, xq, sx, w->w_gate, w->s_gate, w->w_up, w->s_up, nullptr, h};
-  const NormQuant nh{q.T, q.I, q.act, MOE_ROWS_I8, h, nullptr, nullptr, 0.f, nullptr, hq, sh};
+  const I8Product up{q.T, q.H, q.I, MOE_F32, xq, sx, w->w_gate, w->s_gate, w->w_up, w->s_up, nullptr, h};
+  const NormQuant nh{q.T, q.I, MOE_F32, MOE_ROWS_I8, h, nullptr, nullptr, 0.f, nullptr, hq, sh};
   const I8Product down{q.T, q.I, q.H, q.act, hq, sh, w->w_down, w->s_down, nullptr, nullptr, x, x_out};
   MOE_TRY(check_norm_quant(nx));
   MOE_TRY(check_product(up, true));

@@ -4,6 +4,7 @@
 // The sum is exact in int32 (widths are bounded for that), so its order, and with it how
 // the work is split, never changes a result; it becomes fp32 once (exact below 2^24, half
 // an fp32 ulp above), is scaled in fp32 and rounded once to the output type.
+#include "gemm_common.h"
 #include "moe_dense.h"
 
 namespace moe {
@@ -35,13 +36,13 @@ __device__ __forceinline__ void store_out4(TO* y, const TO* res, int64_t row_off
 }
 
 // Few rows: bound by the weight stream.  A workgroup of eight waves owns 16 output columns
-// (of both matrices when gated) and 16 * TB tokens; the waves split K in units of 128 bytes
+// (of both matrices when gated) of every token; the waves split K in units of 128 bytes
 // and meet in LDS.  Weights are the MFMA's A operand and tokens its B operand, both loaded
 // from global memory straight into the registers the matrix core reads: lane l holds row
 // l % 16 and 32 contiguous bytes of a unit at (l / 16) * 32, as two k-slots of a 16x16x64
 // step (which k an MFMA slot stands for is free as long as both operands agree), so a row's
 // unit is one 128-byte line.  Two units per wave are in flight beside the two in use.
-// grid = (ceil(N / 16), ceil(T / (16 TB))), block = 512.
+// T <= 16 TB; grid = ceil(N / 16), block = 512.
 template <typename TO, int TB, bool GLU>
 __global__ __launch_bounds__(512) void k_i8_few(const int8_t* __restrict__ x,
                                                 const float* __restrict__ sx,
@@ -55,14 +56,13 @@ __global__ __launch_bounds__(512) void k_i8_few(const int8_t* __restrict__ x,
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
   const int r16 = lane & 15, q = lane >> 4;
   const int n0 = blockIdx.x * 16;
-  const int64_t t0 = int64_t(blockIdx.y) * (16 * TB);
   const int64_t nrow = int64_t(min(n0 + r16, N - 1)) * K;   // rows past the end: the last one,
   const int8_t* wp[NA];                                      // computed and not stored
   wp[0] = w + nrow;
   if (GLU) wp[NA - 1] = wu + nrow;
   const int8_t* xp[TB];
 #pragma unroll
-  for (int b = 0; b < TB; ++b) xp[b] = x + min<int64_t>(t0 + 16 * b + r16, T - 1) * K;
+  for (int b = 0; b < TB; ++b) xp[b] = x + min<int64_t>(16 * b + r16, T - 1) * K;
 
   i32x4 acc[NA][TB];
 #pragma unroll
@@ -120,7 +120,7 @@ __global__ __launch_bounds__(512) void k_i8_few(const int8_t* __restrict__ x,
 #pragma unroll
       for (int i = 1; i < NW; ++i) s[a] += part[i][a * TB + b][l];
     }
-    const int64_t t = t0 + 16 * b + (l & 15);
+    const int64_t t = 16 * b + (l & 15);
     const int n = n0 + 4 * (l >> 4);
     if (t >= T) continue;
     const float st = sx[t];
@@ -135,23 +135,344 @@ __global__ __launch_bounds__(512) void k_i8_few(const int8_t* __restrict__ x,
   }
 }
 
-template <typename TO, bool GLU>
-static int launch_few(const I8Product& p, bool vec, hipStream_t st) {
-  const int tb = p.T <= 16 ? 1 : p.T <= 32 ? 2 : 4;
-  const int64_t gy = (p.T + 16 * tb - 1) / (16 * tb);
-  auto go = [&](auto kern) {
-    // the second grid dimension ends at 65535: longer batches go in slices of rows
-    for (int64_t y0 = 0; y0 < gy; y0 += 65535) {
-      const int64_t t0 = y0 * 16 * tb, rows = std::min<int64_t>(p.T - t0, int64_t(65535) * 16 * tb);
-      hipLaunchKernelGGL(kern, dim3(unsigned((p.N + 15) / 16), unsigned(std::min<int64_t>(gy - y0, 65535))),
-                         dim3(512), 0, st, p.x + t0 * p.K, p.sx + t0, p.w, p.sw, p.w_up, p.s_up,
-                         p.res ? static_cast<const TO*>(p.res) + t0 * p.N : nullptr,
-                         static_cast<TO*>(p.y) + t0 * p.N, rows, p.K, p.N, vec);
+// 16-byte chunks of the tile's LDS rows are XOR-swizzled so that the 16 consecutive rows one
+// ds_read_b128 serves together at one chunk lie in 16 different 16-byte slots of a bank line.
+template <int BK> __device__ __forceinline__ int i8_swz(int row) {
+  return BK == 64 ? (row >> 2) & 3 : BK == 128 ? (row >> 1) & 7 : row & 15;
+}
+
+#ifndef MOE_I8_GM
+#define MOE_I8_GM 4
+#endif
+// Tile of a workgroup: workgroup b runs on XCD b % 8, every XCD takes one contiguous run of
+// the tiles in an order that walks GM token tiles per weight tile, so that the tiles in flight
+// on an XCD share rows and weights in its L2.
+__device__ __forceinline__ bool i8_tile_item(int mtiles, int ntiles, int& mt, int& nt) {
+  constexpr int GM = MOE_I8_GM;
+  const int n = mtiles * ntiles, per = (n + 7) >> 3;
+  const int j = int(blockIdx.x & 7) * per + int(blockIdx.x >> 3);
+  if (int(blockIdx.x >> 3) >= per || j >= n) return false;
+  const int band = j / (GM * ntiles), first = band * GM;
+  const int rows = min(GM, mtiles - first), in = j - band * GM * ntiles;
+  mt = first + in % rows;
+  nt = in / rows;
+  return true;
+}
+
+// A wave's accumulators -> outputs, through 32-row pieces in LDS that only this wave uses:
+// a lane holds 4 consecutive columns of one token per block, and leaves with 8
+// consecutive columns of a token, so that stores are 16 bytes and contiguous over the lanes.
+template <typename TO, bool GLU, class C>
+__device__ __forceinline__ void i8_epilogue(unsigned char* stg, const i32x4 (&acc)[C::FN][C::FM],
+                                            const float* sx, const float* sw, const float* su,
+                                            const TO* res, TO* y, int64_t T, int N, int64_t tw,
+                                            int nw, bool vec, int lane) {
+  constexpr int RS = C::TN + 4;                       // ints per staged row
+  constexpr int OC = GLU ? C::TN / 2 : C::TN;
+  constexpr int LPR = OC / 8, RPP = 64 / LPR;         // lanes per row, rows per pass
+  int* const st = reinterpret_cast<int*>(stg);
+  const int c8 = (lane % LPR) * 8, n = nw + c8;
+  float s0[8], s1[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    s0[i] = sw[min(n + i, N - 1)];
+    s1[i] = GLU ? su[min(n + i, N - 1)] : 0.f;
+  }
+#pragma unroll
+  for (int m = 0; m < C::FM / 2; ++m) {
+#pragma unroll
+    for (int f = 0; f < C::FN; ++f)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        *reinterpret_cast<i32x4*>(st + (16 * e + (lane & 15)) * RS + f * 16 + 4 * (lane >> 4)) =
+            acc[f][2 * m + e];
+#pragma unroll
+    for (int p = 0; p < 32 / RPP; ++p) {
+      const int row = p * RPP + lane / LPR;
+      const int64_t t = tw + m * 32 + row;
+      const i32x4 a0 = *reinterpret_cast<const i32x4*>(st + row * RS + c8);
+      const i32x4 a1 = *reinterpret_cast<const i32x4*>(st + row * RS + c8 + 4);
+      const float ts = sx[min<int64_t>(t, T - 1)];
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = i8_scaled(i < 4 ? a0[i & 3] : a1[i & 3], ts, s0[i]);
+      if (GLU) {
+        const i32x4 b0 = *reinterpret_cast<const i32x4*>(st + row * RS + OC + c8);
+        const i32x4 b1 = *reinterpret_cast<const i32x4*>(st + row * RS + OC + c8 + 4);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          v[i] = silu(v[i]) * i8_scaled(i < 4 ? b0[i & 3] : b1[i & 3], ts, s1[i]);
+      }
+      if (t >= T || n >= N) continue;
+      const int64_t at = t * N + n;
+      if (vec) {
+        if (res) {
+          float r[8];
+          load8(res + at, r);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] += r[i];
+        }
+        store8(y + at, v);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (n + i < N) y[at + i] = from_f32<TO>(res ? v[i] + to_f32<TO>(res[at + i]) : v[i]);
+      }
+    }
+  }
+}
+
+// Geometry of the tiled kernel: BM tokens x BN weight rows per workgroup (gated: BN / 2 columns
+// of h, each with its gate and its up row), NWM x NWN wave positions, K slabs of BK bytes in a
+// ring of S; at each position KW waves share the slab's K steps (small tiles: more loads in
+// flight per tile) and add their sums at the end.
+template <int BM_, int BN_, int NWM_, int NWN_, int BK_, int S_, int KW_ = 1>
+struct I8Tile {
+  static constexpr int BM = BM_, BN = BN_, NWM = NWM_, NWN = NWN_, BK = BK_, S = S_, KW = KW_;
+  static constexpr int NP = NWM * NWN, NW = NP * KW, TM = BM / NWM, TN = BN / NWN;   // a wave's part
+  static constexpr int FM = TM / 16, FN = TN / 16, FH = FM / 2;        // 16x16 blocks of it
+  static constexpr int KS = BK / 64 / KW;                              // MFMA steps per slab and wave
+  static constexpr int CPR = BK / 16;                                  // 16-byte chunks per row
+  static constexpr int SLAB = (BM + BN) * BK;                          // bytes
+  static constexpr int L = SLAB / 1024 / NW;                           // loads per lane and slab
+  static constexpr int STG = 32 * (TN + 4) * 4;                        // epilogue bytes per wave
+  static constexpr int RED = FM * FN * 1024;                           // a wave's sums
+  static constexpr int END = NP * (STG > (KW - 1) * RED ? STG : (KW - 1) * RED);
+  static constexpr int LDS = S * SLAB > END ? S * SLAB : END;
+  static_assert(L * NW * 1024 == SLAB && S >= 2 && FM % 2 == 0 && KS >= 1 && LDS <= 163840,
+                "tile geometry");
+};
+
+// All but the N newest loads of this wave have landed and its LDS reads are done, then the
+// workgroup meets.  The fences keep the compiler from moving LDS accesses across either.
+template <int N>
+__device__ __forceinline__ void i8_slab_sync() {
+  asm volatile("" ::: "memory");
+  wait_vm_lgkm0<N>();
+  block_sync_nowait();
+}
+
+// The tiled product.  Tokens are the MFMA's B operand and weights its A operand, so that a
+// lane ends with four consecutive columns of one token; 16x16x64 steps, because at this card's
+// power limit they run faster on data than 32x32x32 (register-only loop, all CUs: 4.2e15
+// against 3.5e15 op/s; 4.8e15 for both on zeros).
+// Both operands move global -> LDS by direct 16-byte loads, a 128-byte line per row and slab
+// (with 64-byte slabs the loads alone ran at 28 instead of 40 bytes per clock and CU).  A slab's
+// slot is refilled as soon as the last fragments of it are in registers, half a phase before
+// the slab's end, which is also where the one barrier per slab is; each phase's fragments are
+// read during the phase before.
+// 8192 x 4096 x 8192: 233 us, 2.35e15 op/s; 8192 x 8192 x 2048: 111 us, 2.47e15.
+template <typename TO, bool GLU, class C>
+__global__ __launch_bounds__(C::NW * 64) void k_i8_tile(const int8_t* __restrict__ x,
+                                                        const float* __restrict__ sx,
+                                                        const int8_t* __restrict__ w,
+                                                        const float* __restrict__ sw,
+                                                        const int8_t* __restrict__ wu,
+                                                        const float* __restrict__ su,
+                                                        const TO* res, TO* y, int64_t T, int K,
+                                                        int N, int mtiles, int ntiles, bool vec) {
+  constexpr int OC = GLU ? C::TN / 2 : C::TN;              // output columns per wave
+  __shared__ __align__(16) unsigned char lds[C::LDS];
+  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+  const int pos = wv % C::NP, kw = wv / C::NP;
+  const int wm = pos / C::NWN, wn = pos % C::NWN;
+  int mt, nt;
+  if (!i8_tile_item(mtiles, ntiles, mt, nt)) return;
+  const int64_t t0 = int64_t(mt) * C::BM;
+  const int n0 = nt * (GLU ? C::BN / 2 : C::BN);
+
+  // one load instruction of a wave fills 64 / CPR rows; lane L writes chunk position L % CPR
+  const int8_t* src[C::L];
+  int kc[C::L];
+#pragma unroll
+  for (int i = 0; i < C::L; ++i) {
+    const int r = (wv + C::NW * i) * (64 / C::CPR) + lane / C::CPR;
+    kc[i] = ((lane % C::CPR) ^ i8_swz<C::BK>(r)) * 16;
+    if (r < C::BM) {
+      src[i] = x + min<int64_t>(t0 + r, T - 1) * K;
+    } else {
+      const int q = r - C::BM;
+      if (GLU) {
+        const int s = q % C::TN;
+        const int n = min(n0 + q / C::TN * OC + s % OC, N - 1);
+        src[i] = (s < OC ? w : wu) + int64_t(n) * K;
+      } else {
+        src[i] = w + int64_t(min(n0 + q, N - 1)) * K;
+      }
+    }
+  }
+  const int nk = (K + C::BK - 1) / C::BK;
+  auto issue = [&](int kt, int slot) {
+#pragma unroll
+    for (int i = 0; i < C::L; ++i)
+      dma16(src[i] + min(kt * C::BK + kc[i], K - 16), lds + slot * C::SLAB + (wv + C::NW * i) * 1024);
+  };
+
+  i32x4 acc[C::FN][C::FM];
+#pragma unroll
+  for (int n = 0; n < C::FN; ++n)
+#pragma unroll
+    for (int m = 0; m < C::FM; ++m) acc[n][m] = i32x4{0, 0, 0, 0};
+
+  const int l16 = lane & 15, q = lane >> 4;
+  int foff[C::KS];                                       // this lane's chunk of each MFMA step
+#pragma unroll
+  for (int s = 0; s < C::KS; ++s) foff[s] = l16 * C::BK + ((4 * (kw * C::KS + s) + q) ^ i8_swz<C::BK>(l16)) * 16;
+  const unsigned char* const xrow = lds + wm * C::TM * C::BK;
+  const unsigned char* const wrow = lds + (C::BM + wn * C::TN) * C::BK;
+  i32x4 fx[2][C::FH], fw[2][C::FN];
+  auto read_w = [&](int slot, int s, int buf) {
+#pragma unroll
+    for (int n = 0; n < C::FN; ++n)
+      fw[buf][n] = *reinterpret_cast<const i32x4*>(wrow + slot * C::SLAB + foff[s] + n * 16 * C::BK);
+  };
+  auto read_x = [&](int slot, int s, int kt, int half) {
+#pragma unroll
+    for (int m = 0; m < C::FH; ++m)
+      fx[half][m] = *reinterpret_cast<const i32x4*>(xrow + slot * C::SLAB + foff[s] +
+                                                    (half * C::FH + m) * 16 * C::BK);
+    if (kt == nk - 1 && kt * C::BK + (4 * (kw * C::KS + s) + q) * 16 >= K) {   // past K: x counts as zero
+#pragma unroll
+      for (int m = 0; m < C::FH; ++m) fx[half][m] = i32x4{0, 0, 0, 0};
     }
   };
-  if (tb == 1) go(k_i8_few<TO, 1, GLU>);
-  else if (tb == 2) go(k_i8_few<TO, 2, GLU>);
-  else go(k_i8_few<TO, 4, GLU>);
+  auto mul = [&](int half, int buf) {
+#pragma unroll
+    for (int m = 0; m < C::FH; ++m)
+#pragma unroll
+      for (int n = 0; n < C::FN; ++n)
+        acc[n][half * C::FH + m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(
+            fw[buf][n], fx[half][m], acc[n][half * C::FH + m], 0, 0, 0);
+  };
+
+  for (int k = 0; k < C::S; ++k)
+    if (k < nk) issue(k, k);
+  if (nk >= C::S) i8_slab_sync<(C::S - 1) * C::L>(); else i8_slab_sync<0>();
+  read_w(0, 0, 0);
+  read_x(0, 0, 0, 0);
+  int slot = 0;
+  // One slab; WB: buffer its first weight fragments are in.  Every phase multiplies half of
+  // the wave's tokens while the next phase's fragments are read.
+  auto slab = [&](int kt, auto wb) {
+    constexpr int WB = decltype(wb)::value;
+    const int next = slot + 1 == C::S ? 0 : slot + 1;
+#pragma unroll
+    for (int s = 0; s < C::KS; ++s) {
+      read_x(slot, s, kt, 1);
+      mul(0, (WB + s) & 1);
+      if (s + 1 < C::KS) {
+        read_w(slot, s + 1, (WB + s + 1) & 1);
+        read_x(slot, s + 1, kt, 0);
+      } else if (kt + 1 < nk) {
+        // every fragment of this slab is in registers: once all waves are here its slot is
+        // free, and slab kt + 1 (older than the S - 2 slabs that may still be on their way)
+        // can be read
+        if (kt + C::S <= nk) i8_slab_sync<(C::S - 2) * C::L>(); else i8_slab_sync<0>();
+        if (kt + C::S < nk) issue(kt + C::S, slot);
+        read_w(next, 0, (WB + s + 1) & 1);
+        read_x(next, 0, kt + 1, 0);
+      }
+      mul(1, (WB + s) & 1);
+    }
+    slot = next;
+  };
+  if constexpr (C::KS % 2 == 0) {
+    for (int kt = 0; kt < nk; ++kt) slab(kt, std::integral_constant<int, 0>());
+  } else {
+    int kt = 0;
+    for (; kt + 1 < nk; kt += 2) {
+      slab(kt, std::integral_constant<int, 0>());
+      slab(kt + 1, std::integral_constant<int, 1>());
+    }
+    if (kt < nk) slab(kt, std::integral_constant<int, 0>());
+  }
+  i8_slab_sync<0>();               // the ring becomes the waves' own staging memory
+  if constexpr (C::KW > 1) {
+    i32x4* const red = reinterpret_cast<i32x4*>(lds) + lane;
+    if (kw > 0) {
+#pragma unroll
+      for (int n = 0; n < C::FN; ++n)
+#pragma unroll
+        for (int m = 0; m < C::FM; ++m)
+          red[(((kw - 1) * C::NP + pos) * C::FM * C::FN + n * C::FM + m) * 64] = acc[n][m];
+    }
+    __syncthreads();
+    if (kw == 0) {
+#pragma unroll
+      for (int k = 0; k < C::KW - 1; ++k)
+#pragma unroll
+        for (int n = 0; n < C::FN; ++n)
+#pragma unroll
+          for (int m = 0; m < C::FM; ++m)
+            acc[n][m] += red[((k * C::NP + pos) * C::FM * C::FN + n * C::FM + m) * 64];
+    }
+    __syncthreads();
+    if (kw > 0) return;
+  }
+  i8_epilogue<TO, GLU, C>(lds + pos * C::STG, acc, sx, sw, su, res, y, T, N, t0 + wm * C::TM,
+                          n0 + wn * OC, vec, lane);
+}
+
+template <typename TO, bool GLU, int TB>
+static void launch_few(const I8Product& p, bool vec, hipStream_t st) {
+  hipLaunchKernelGGL((k_i8_few<TO, TB, GLU>), dim3(unsigned((p.N + 15) / 16)), dim3(512), 0, st, p.x,
+                     p.sx, p.w, p.sw, p.w_up, p.s_up, static_cast<const TO*>(p.res),
+                     static_cast<TO*>(p.y), p.T, p.K, p.N, vec);
+}
+
+template <typename TO, bool GLU, class C>
+static void launch_tile(const I8Product& p, bool vec, hipStream_t st) {
+  const int64_t mt = (p.T + C::BM - 1) / C::BM, oc = GLU ? C::BN / 2 : C::BN;
+  const int64_t nt = (p.N + oc - 1) / oc;
+  hipLaunchKernelGGL((k_i8_tile<TO, GLU, C>), dim3(xcd_grid(mt * nt)), dim3(C::NW * 64), 0, st, p.x,
+                     p.sx, p.w, p.sw, p.w_up, p.s_up, static_cast<const TO*>(p.res),
+                     static_cast<TO*>(p.y), p.T, p.K, p.N, int(mt), int(nt), vec);
+}
+
+// The tiles: one workgroup of the largest per CU, two or three of the smaller ones.
+using Tile256 = I8Tile<256, 256, 2, 4, 128, 2>;
+using Tile128 = I8Tile<128, 128, 2, 4, 128, 2>;
+using Tile64 = I8Tile<64, 64, 2, 2, 256, 2, 2>;
+using Tile32 = I8Tile<32, 64, 1, 2, 256, 2, 4>;
+
+// Which kernel: up to 16 tokens (32 without the gate) the weights are streamed past every
+// token at once; beyond, the tile whose estimated time is least.  The estimate is
+//   (tiles per CU) * (128-wide K slabs) * (time per slab and tile) + (start and end),
+// fitted to measurements from 64 to 8192 tokens (us: slab 0.14 / 0.22 / 0.6 / 1.63, start
+// and end 3.4 / 4.2 / 5 / 6 for 32x64, 64x64, 128x128, 256x256).  The smaller tiles share a CU,
+// so a part of a round costs a part of it; the largest pays whole rounds, ends included.
+// Measured on either side of a switch (us): 64 x 1536 x 4096 few 5.9, 32x64 5.1; 512 x 2048 x
+// 2048 32x64 7.6, 64x64 7.3, 128x128 13.9; 2048 x 2048 x 2048 64x64 19.5, 128x128 16.5;
+// 8192 x 8192 x 2048 128x128 152, 256x256 111.
+template <typename TO, bool GLU>
+static int launch_product(const I8Product& p, bool vec, hipStream_t st) {
+  if (p.T <= 16) {
+    launch_few<TO, GLU, 1>(p, vec, st);
+    return check_launch();
+  }
+  if constexpr (!GLU) {
+    if (p.T <= 32) {
+      launch_few<TO, GLU, 2>(p, vec, st);
+      return check_launch();
+    }
+  }
+  const double slabs = double((p.K + 127) / 128);
+  auto tiles = [&](int bm, int bn) {
+    const int oc = GLU ? bn / 2 : bn;
+    return double((p.T + bm - 1) / bm) * double((p.N + oc - 1) / oc) / 256.0;
+  };
+  const double e256 = std::ceil(tiles(256, 256)) * (slabs * 1.63 + 6.0);
+  const double e128 = std::max(1.0, tiles(128, 128)) * slabs * 0.6 + 5.0;
+  const double e64 = std::max(1.0, tiles(64, 64)) * slabs * 0.22 + 4.2;
+  const double e32 = std::max(1.0, tiles(32, 64)) * slabs * 0.14 + 3.4;
+  if (e256 <= std::min(e128, std::min(e64, e32)))
+    launch_tile<TO, GLU, Tile256>(p, vec, st);
+  else if (e128 <= std::min(e64, e32))
+    launch_tile<TO, GLU, Tile128>(p, vec, st);
+  else if (e64 <= e32)
+    launch_tile<TO, GLU, Tile64>(p, vec, st);
+  else
+    launch_tile<TO, GLU, Tile32>(p, vec, st);
   return check_launch();
 }
 
@@ -159,8 +480,8 @@ int launch_i8_product(const I8Product& p, hipStream_t st) {
   auto aligned = [](const void* a) { return (reinterpret_cast<uintptr_t>(a) & 15) == 0; };
   const bool vec = p.N % 8 == 0 && aligned(p.y) && (!p.res || aligned(p.res));
   if (p.out == MOE_F32)
-    return p.w_up ? launch_few<float, true>(p, vec, st) : launch_few<float, false>(p, vec, st);
-  return p.w_up ? launch_few<bf16_t, true>(p, vec, st) : launch_few<bf16_t, false>(p, vec, st);
+    return p.w_up ? launch_product<float, true>(p, vec, st) : launch_product<float, false>(p, vec, st);
+  return p.w_up ? launch_product<bf16_t, true>(p, vec, st) : launch_product<bf16_t, false>(p, vec, st);
 }
 
 }  // namespace moe

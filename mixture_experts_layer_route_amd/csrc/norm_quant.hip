@@ -61,9 +61,12 @@ __global__ __launch_bounds__(WPR == 16 ? 1024 : 256) void k_norm_quant(
   if (gamma) {
     float ss = 0.f;
 #pragma unroll
-    for (int j = 0; j < NCH; ++j)
+    for (int j = 0; j < NCH; ++j) {
+      float sj = v[j][0] * v[j][0];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(v[j][i], v[j][i], ss);
+      for (int i = 1; i < 8; ++i) sj = fmaf(v[j][i], v[j][i], sj);
+      ss += sj;
+    }
     ss = wave_sum(ss);
     if (WPR > 1) {
       if (lane == 0) part[wv] = ss;
@@ -72,7 +75,8 @@ __global__ __launch_bounds__(WPR == 16 ? 1024 : 256) void k_norm_quant(
 #pragma unroll
       for (int i = 0; i < WPR; ++i) ss += part[wv / WPR * WPR + i];
     }
-    const float rinv = 1.0f / sqrtf(ss / float(H) + eps);
+    // once per row, in 64 bits: an error here would shift every code of the row
+    const float rinv = float(1.0 / sqrt(double(ss) / H + double(eps)));
 #pragma unroll
     for (int j = 0; j < NCH; ++j) {
       const int c = j * 64 * WPR + pos;

@@ -6,8 +6,8 @@ shared with the library.  A dense layer stands beside the MoE blocks in the stac
 TensorFold issue #1247 describes (config paragraph: 24 layers, a dense layer 0); its 8-bit
 form is the usual one of int8 codes with a scale per token and per output channel.
 
-Nothing is rounded except what the operators store: the residual sum, rows, h and outputs in
-the activation type, and the codes.
+Nothing is rounded except what the operators store: the residual sum, rows and outputs in the
+activation type, and the codes.
 """
 from __future__ import annotations
 
@@ -47,8 +47,8 @@ def glu(x_codes, x_scales, w_gate, s_gate, w_up, s_up) -> np.ndarray:
 
 
 def dense_layer(x, gamma, w, act="bf16", eps=mo.RMS_EPS) -> np.ndarray:
-    """x + down(i8(round(glu(i8(norm(x)))))), before the store's rounding.  `w`: codes w_gate,
+    """x + down(i8(glu(i8(norm(x))))), before the store's rounding.  `w`: codes w_gate,
     w_up, w_down and scales s_gate, s_up, s_down."""
     xq, sx = quant_i8(norm_rows(x, gamma, None, eps, act))
-    h = mo.round_act(glu(xq, sx, w["w_gate"], w["s_gate"], w["w_up"], w["s_up"]), act)
+    h = glu(xq, sx, w["w_gate"], w["s_gate"], w["w_up"], w["s_up"])
     return np.asarray(x, dtype=np.float64) + product(*quant_i8(h), w["w_down"], w["s_down"])

@@ -97,7 +97,7 @@ BAD_PRODUCT = [
     (-1, dict(w=None)), (-1, dict(sw=None)), (-1, dict(y=None)), (-1, dict(x=FAKE + 8)),
     (-1, dict(w=FAKE + 1)), (-1, dict(sx=FAKE + 2)), (-1, dict(sw=FAKE + 1)), (-1, dict(y=FAKE + 1)),
     (-1, dict(out=0, y=FAKE + 2)), (-2, dict(out=2)), (-2, dict(K=1544)), (-2, dict(K=65552)),
-    (-2, dict(rows=1 << 31)), (-2, dict(N=(1 << 30) + 1)),
+    (-2, dict(rows=1 << 31)), (-2, dict(N=(1 << 30) + 1)), (-2, dict(rows=1 << 25, N=(1 << 15) + 1)),
 ]
 
 
