@@ -49,7 +49,8 @@ static int check_product(const I8Product& p, bool glu) {
 struct DensePlan {
   int64_t T;
   int H, I, act;
-  size_t o_xq, o_sx, o_h, o_hq, o_sh, total;
+  bool few;                // up to 16 tokens: codes never leave the kernels
+  size_t o_xq, o_sx, o_h, o_hq, o_sh, o_hmax, total;
 };
 
 static int make_dense_plan(const moe_dense_config* c, DensePlan* out) {
@@ -66,11 +67,13 @@ static int make_dense_plan(const moe_dense_config* c, DensePlan* out) {
   q.act = c->act_dtype;
   size_t o = 0;
   auto take = [&](size_t bytes) { const size_t at = o; o = align256(o + bytes); return at; };
-  q.o_xq = take(size_t(q.T) * q.H);
-  q.o_sx = take(size_t(q.T) * 4);
+  q.few = dense_few_ok(q.T, q.H, q.I);
+  q.o_xq = take(q.few ? 0 : size_t(q.T) * q.H);
+  q.o_sx = take(q.few ? 0 : size_t(q.T) * 4);
   q.o_h = take(size_t(q.T) * q.I * 4);   // fp32: h is rounded once, to its codes
-  q.o_hq = take(size_t(q.T) * q.I);
-  q.o_sh = take(size_t(q.T) * 4);
+  q.o_hq = take(q.few ? 0 : size_t(q.T) * q.I);
+  q.o_sh = take(q.few ? 0 : size_t(q.T) * 4);
+  q.o_hmax = take(q.few ? dense_few_hmax_bytes(q.T, q.I) : 0);
   q.total = o;
   *out = q;
   return MOE_OK;
@@ -120,7 +123,7 @@ int moe_dense_residual_i8(const moe_dense_config* cfg, const void* x, const void
   DensePlan q;
   MOE_TRY(make_dense_plan(cfg, &q));
   if (!x || !norm_weight || !w || !x_out || !ws || !(norm_eps >= 0.f)) return MOE_ERR_ARG;
-  if ((reinterpret_cast<uintptr_t>(ws) & 255) != 0) return MOE_ERR_ARG;
+  if ((reinterpret_cast<uintptr_t>(ws) & 255) != 0 || !aligned16(x_out)) return MOE_ERR_ARG;
   if (ws_bytes < q.total) return MOE_ERR_WORKSPACE;
   char* base = static_cast<char*>(ws);
   int8_t* xq = reinterpret_cast<int8_t*>(base + q.o_xq);
@@ -136,6 +139,11 @@ int moe_dense_residual_i8(const moe_dense_config* cfg, const void* x, const void
   MOE_TRY(check_product(up, true));
   MOE_TRY(check_norm_quant(nh));
   MOE_TRY(check_product(down, false));
+  if (q.few) {
+    const DenseFew d{q.T, q.H, q.I, q.act, x, norm_weight, norm_eps, w, static_cast<float*>(h),
+                     reinterpret_cast<float*>(base + q.o_hmax), x_out};
+    return launch_dense_few(d, stream);
+  }
   MOE_TRY(launch_norm_quant(nx, stream));
   MOE_TRY(launch_i8_product(up, stream));
   MOE_TRY(launch_norm_quant(nh, stream));

@@ -35,54 +35,212 @@ __device__ __forceinline__ void store_out4(TO* y, const TO* res, int64_t row_off
     if (n + r < N) y[row_off + n + r] = from_f32<TO>(v[r]);
 }
 
+// What a kernel of this file reads and writes.  One argument by value: on the host a launch
+// costs about 0.1 us per kernel argument (2.9 us for this struct, 3.9 us for twelve arguments),
+// which is what the smallest calls are made of.
+struct I8Args {
+  const int8_t* x;         // [T, K] codes and
+  const float* sx;         // [T] scales (unless the kernel makes them itself)
+  const int8_t* w;         // [N, K], [N]
+  const float* sw;
+  const int8_t* wu;        // the up matrix of a gated product
+  const float* su;
+  const void* res;         // [T, N] or null
+  void* y;                 // [T, N]
+  int64_t T;
+  int K, N;
+  int mtiles, ntiles;      // tiled kernel
+  int vec;                 // rows of y and res are 16-byte aligned and N % 8 == 0
+  // sources of the kernels that make their own codes
+  const void* rows;        // kNorm: [T, K] activation rows; kQuant: h, fp32 [T, K]
+  const void* gamma;       // kNorm: [K]
+  float eps;
+  float* hmax;             // [T, tiles of 16 columns]: largest |h| of a tile, out (kNorm) or in (kQuant)
+};
+
+// Where a few-row kernel's token codes come from: memory; or made by every workgroup for
+// itself in LDS, from activation rows (RMSNorm in front) or from the fp32 h of the gated product.
+enum FewSrc { kCodes, kNorm, kQuant };
+
+constexpr int kFewCodes = 128 << 10;     // LDS bytes of codes a workgroup may make
+
+// LDS row stride of the codes: 16 tokens' equal chunks fall on 16 different bank groups
+// (a row is a whole number of 256-byte bank lines for the usual widths).
+__host__ __device__ inline int few_stride(int K) { return (K + 255) / 256 * 256 + 16; }
+
+// RMSNorm and int8 codes of the rows wv, wv + 8 in LDS, by the definitions of k_norm_quant; a
+// wave per row with NCH chunks of 8 elements per lane (K <= 512 NCH).  load() only issues
+// loads, so that the weights' can follow before the first value is waited for.
+template <typename TA, int NCH>
+struct FewNorm {
+  Chunk8<TA> x[2][NCH], g[NCH];
+  __device__ __forceinline__ void load(const I8Args& a, int lane, int wv) {
+#pragma unroll
+    for (int j = 0; j < NCH; ++j) {
+      const int c = j * 64 + lane;
+      if (c < a.K / 8) {
+        if (wv < a.T) g[j].load(static_cast<const TA*>(a.gamma) + c * 8);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (wv + 8 * i < a.T)
+            x[i][j].load(static_cast<const TA*>(a.rows) + int64_t(wv + 8 * i) * a.K + c * 8);
+      }
+    }
+  }
+  __device__ __forceinline__ void store(const I8Args& a, int lane, int wv, int8_t* codes, float* sx) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int t = wv + 8 * i;
+      if (t >= a.T) break;                   // uniform over the wave
+      float v[NCH][8], ss = 0.f;
+#pragma unroll
+      for (int j = 0; j < NCH; ++j) {
+        if (j * 64 + lane < a.K / 8) {
+          x[i][j].get(v[j]);
+          float sj = v[j][0] * v[j][0];
+#pragma unroll
+          for (int e = 1; e < 8; ++e) sj = fmaf(v[j][e], v[j][e], sj);
+          ss += sj;
+        }
+      }
+      const float rinv = float(1.0 / sqrt(double(wave_sum(ss)) / a.K + double(a.eps)));
+      float m = 0.f;
+#pragma unroll
+      for (int j = 0; j < NCH; ++j)
+        if (j * 64 + lane < a.K / 8) {
+          float gv[8];
+          g[j].get(gv);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            v[j][e] = v[j][e] * rinv * gv[e];
+            m = fmaxf(m, fabsf(v[j][e]));
+          }
+        }
+      const float scale = i8_scale(wave_max(m));
+      if (lane == 0) sx[t] = scale;
+#pragma unroll
+      for (int j = 0; j < NCH; ++j) {
+        const int c = j * 64 + lane;
+        if (c < a.K / 8) *reinterpret_cast<uint2*>(codes + t * few_stride(a.K) + c * 8) = i8x8(v[j], scale);
+      }
+    }
+  }
+};
+
+// int8 codes of h in LDS: the 8 waves share the rows (all eight on one row, four on each of
+// two, two on each of four, one on each of eight, two rows each beyond).  A row's largest value
+// comes from its tiles' maxima, so h is read once; a lane's first chunks and maxima are on
+// their way before the weights.
+struct FewQuant {
+  static constexpr int PRE = 2, HM = 6;
+  Chunk8<float> h[2][PRE];
+  float hm[2][HM];
+  int wpr;
+  __device__ __forceinline__ void load(const I8Args& a, int lane, int wv) {
+    wpr = a.T == 1 ? 8 : a.T == 2 ? 4 : a.T <= 4 ? 2 : 1;
+    const int nt = (a.K + 15) / 16;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int t = wv / wpr + 8 / wpr * i;
+      if (t >= a.T) break;                   // uniform over the wave
+#pragma unroll
+      for (int j = 0; j < HM; ++j)
+        hm[i][j] = a.hmax[int64_t(t) * nt + min(j * 64 + lane, nt - 1)];
+#pragma unroll
+      for (int j = 0; j < PRE; ++j) {
+        const int c = j * 64 * wpr + (wv % wpr) * 64 + lane;
+        if (c < a.K / 8) h[i][j].load(static_cast<const float*>(a.rows) + int64_t(t) * a.K + c * 8);
+      }
+    }
+  }
+  __device__ __forceinline__ void store(const I8Args& a, int lane, int wv, int8_t* codes, float* sx) {
+    const int nt = (a.K + 15) / 16;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int t = wv / wpr + 8 / wpr * i;
+      if (t >= a.T) break;
+      float m = 0.f;
+#pragma unroll
+      for (int j = 0; j < HM; ++j) m = fmaxf(m, hm[i][j]);
+      for (int c = HM * 64 + lane; c < nt; c += 64) m = fmaxf(m, a.hmax[int64_t(t) * nt + c]);
+      const float scale = i8_scale(wave_max(m));
+      if (lane == 0) sx[t] = scale;          // (the waves of a row write the same value)
+      int8_t* const row = codes + t * few_stride(a.K);
+#pragma unroll
+      for (int j = 0; j < PRE; ++j) {
+        const int c = j * 64 * wpr + (wv % wpr) * 64 + lane;
+        float v[8];
+        h[i][j].get(v);
+        if (c < a.K / 8) *reinterpret_cast<uint2*>(row + c * 8) = i8x8(v, scale);
+      }
+      for (int c = PRE * 64 * wpr + (wv % wpr) * 64 + lane; c < a.K / 8; c += 64 * wpr) {
+        float v[8];
+        load8(static_cast<const float*>(a.rows) + int64_t(t) * a.K + c * 8, v);
+        *reinterpret_cast<uint2*>(row + c * 8) = i8x8(v, scale);
+      }
+    }
+  }
+};
+struct FewNone {
+  __device__ __forceinline__ void load(const I8Args&, int, int) {}
+  __device__ __forceinline__ void store(const I8Args&, int, int, int8_t*, float*) {}
+};
+
 // Few rows: bound by the weight stream.  A workgroup of eight waves owns 16 output columns
 // (of both matrices when gated) of every token; the waves split K in units of 128 bytes
-// and meet in LDS.  Weights are the MFMA's A operand and tokens its B operand, both loaded
-// from global memory straight into the registers the matrix core reads: lane l holds row
-// l % 16 and 32 contiguous bytes of a unit at (l / 16) * 32, as two k-slots of a 16x16x64
-// step (which k an MFMA slot stands for is free as long as both operands agree), so a row's
-// unit is one 128-byte line.  Two units per wave are in flight beside the two in use.
-// T <= 16 TB; grid = ceil(N / 16), block = 512.
-template <typename TO, int TB, bool GLU>
-__global__ __launch_bounds__(512) void k_i8_few(const int8_t* __restrict__ x,
-                                                const float* __restrict__ sx,
-                                                const int8_t* __restrict__ w,
-                                                const float* __restrict__ sw,
-                                                const int8_t* __restrict__ wu,
-                                                const float* __restrict__ su, const TO* res, TO* y,
-                                                int64_t T, int K, int N, bool vec) {
+// and meet in LDS.  Weights are the MFMA's A operand and tokens its B operand, weights (and
+// codes that lie in memory) loaded straight into the registers the matrix core reads: lane l
+// holds row l % 16 and 32 contiguous bytes of a unit at (l / 16) * 32, as two k-slots of a
+// 16x16x64 step (which k an MFMA slot stands for is free as long as both operands agree), so a
+// row's unit is one 128-byte line.  Two units per wave are in flight while codes are made and
+// beside the two in use.
+// T <= 16 TB; grid = ceil(N / 16), block = 512, dynamic LDS = T * few_stride(K) unless kCodes.
+template <typename TO, int TB, bool GLU, FewSrc SRC, class Make>
+__global__ __launch_bounds__(512) void k_i8_few(I8Args a) {
   constexpr int NW = 8, NA = GLU ? 2 : 1;
   __shared__ i32x4 part[NW][NA * TB][64];
+  __shared__ float own_sx[16];
+  extern __shared__ __align__(16) int8_t own_codes[];
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
   const int r16 = lane & 15, q = lane >> 4;
   const int n0 = blockIdx.x * 16;
+  const int K = a.K, N = a.N;
+  const int T = int(a.T);
   const int64_t nrow = int64_t(min(n0 + r16, N - 1)) * K;   // rows past the end: the last one,
   const int8_t* wp[NA];                                      // computed and not stored
-  wp[0] = w + nrow;
-  if (GLU) wp[NA - 1] = wu + nrow;
+  wp[0] = a.w + nrow;
+  if (GLU) wp[NA - 1] = a.wu + nrow;
   const int8_t* xp[TB];
 #pragma unroll
-  for (int b = 0; b < TB; ++b) xp[b] = x + min<int64_t>(16 * b + r16, T - 1) * K;
+  for (int b = 0; b < TB; ++b) {
+    const int t = min(16 * b + r16, T - 1);
+    xp[b] = SRC == kCodes ? a.x + int64_t(t) * K : own_codes + t * few_stride(K);
+  }
 
   i32x4 acc[NA][TB];
 #pragma unroll
-  for (int a = 0; a < NA; ++a)
+  for (int i = 0; i < NA; ++i)
 #pragma unroll
-    for (int b = 0; b < TB; ++b) acc[a][b] = i32x4{0, 0, 0, 0};
+    for (int b = 0; b < TB; ++b) acc[i][b] = i32x4{0, 0, 0, 0};
 
-  struct Unit { i32x4 a[NA][2], b[TB][2]; };
+  struct Unit { i32x4 w[NA][2], x[TB][2]; };
   const int nu = (K + 127) >> 7;
-  auto load = [&](int u, Unit& f) {
+  auto load_w = [&](int u, Unit& f) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int ko = min(u * 128 + q * 32 + h * 16, K - 16);   // chunks past K: a valid address
+#pragma unroll
+      for (int i = 0; i < NA; ++i) f.w[i][h] = *reinterpret_cast<const i32x4*>(wp[i] + ko);
+    }
+  };
+  auto load_x = [&](int u, Unit& f) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int k = u * 128 + q * 32 + h * 16;
-      const int ko = min(k, K - 16);               // chunks past K: a valid address, x as zeros
-#pragma unroll
-      for (int a = 0; a < NA; ++a) f.a[a][h] = *reinterpret_cast<const i32x4*>(wp[a] + ko);
 #pragma unroll
       for (int b = 0; b < TB; ++b) {
-        f.b[b][h] = *reinterpret_cast<const i32x4*>(xp[b] + ko);
-        if (k >= K) f.b[b][h] = i32x4{0, 0, 0, 0};
+        f.x[b][h] = *reinterpret_cast<const i32x4*>(xp[b] + min(k, K - 16));
+        if (k >= K) f.x[b][h] = i32x4{0, 0, 0, 0};             // ... that counts as zero
       }
     }
   };
@@ -90,49 +248,75 @@ __global__ __launch_bounds__(512) void k_i8_few(const int8_t* __restrict__ x,
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int a = 0; a < NA; ++a)
+      for (int i = 0; i < NA; ++i)
 #pragma unroll
         for (int b = 0; b < TB; ++b)
-          acc[a][b] = __builtin_amdgcn_mfma_i32_16x16x64_i8(f.a[a][h], f.b[b][h], acc[a][b], 0, 0, 0);
+          acc[i][b] = __builtin_amdgcn_mfma_i32_16x16x64_i8(f.w[i][h], f.x[b][h], acc[i][b], 0, 0, 0);
   };
   Unit f0, f1;
   int u = wv;
-  if (u < nu) load(u, f0);
-  for (; u < nu; u += 2 * NW) {
-    if (u + NW < nu) load(u + NW, f1);
+  Make make;
+  make.load(a, lane, wv);
+  if (u < nu) load_w(u, f0);
+  if (SRC == kCodes) {
+    if (u < nu) load_x(u, f0);
+  } else {
+    if (u + NW < nu) load_w(u + NW, f1);
+    make.store(a, lane, wv, own_codes, own_sx);
+    __syncthreads();
+  }
+  for (bool first = true; u < nu; u += 2 * NW, first = false) {
+    if (SRC != kCodes) load_x(u, f0);
+    if (u + NW < nu) {
+      if (SRC == kCodes || !first) load_w(u + NW, f1);
+      if (SRC == kCodes) load_x(u + NW, f1);
+    }
     mul(f0);
-    if (u + 2 * NW < nu) load(u + 2 * NW, f0);
-    if (u + NW < nu) mul(f1);
+    if (u + 2 * NW < nu) {
+      load_w(u + 2 * NW, f0);
+      if (SRC == kCodes) load_x(u + 2 * NW, f0);
+    }
+    if (u + NW < nu) {
+      if (SRC != kCodes) load_x(u + NW, f1);
+      mul(f1);
+    }
   }
 
 #pragma unroll
-  for (int a = 0; a < NA; ++a)
+  for (int i = 0; i < NA; ++i)
 #pragma unroll
-    for (int b = 0; b < TB; ++b) part[wv][a * TB + b][lane] = acc[a][b];
+    for (int b = 0; b < TB; ++b) part[wv][i * TB + b][lane] = acc[i][b];
   __syncthreads();
-  // one thread per four outputs: columns n .. n+3 of token t
-  for (int e = threadIdx.x; e < TB * 64; e += 512) {
-    const int b = e >> 6, l = e & 63;
-    i32x4 s[NA];
+  // a wave per 16 tokens, a thread per four outputs: columns n .. n + 3 of token t
+  if (wv >= TB) return;
+  const int b = wv, n = n0 + 4 * q;
+  const int t = 16 * b + r16;
+  i32x4 s[NA];
 #pragma unroll
-    for (int a = 0; a < NA; ++a) {
-      s[a] = part[0][a * TB + b][l];
+  for (int i = 0; i < NA; ++i) {
+    s[i] = part[0][i * TB + b][lane];
 #pragma unroll
-      for (int i = 1; i < NW; ++i) s[a] += part[i][a * TB + b][l];
-    }
-    const int64_t t = 16 * b + (l & 15);
-    const int n = n0 + 4 * (l >> 4);
-    if (t >= T) continue;
-    const float st = sx[t];
-    float v[4];
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int nr = min(n + r, N - 1);
-      v[r] = i8_scaled(s[0][r], st, sw[nr]);
-      if (GLU) v[r] = silu(v[r]) * i8_scaled(s[NA - 1][r], st, su[nr]);
-    }
-    store_out4<TO>(y, res, t * N, n, N, vec, v);
+    for (int k = 1; k < NW; ++k) s[i] += part[k][i * TB + b][lane];
   }
+  const float st = SRC == kCodes ? a.sx[min(t, T - 1)] : own_sx[min(t, T - 1)];
+  float v[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int nr = min(n + r, N - 1);
+    v[r] = i8_scaled(s[0][r], st, a.sw[nr]);
+    if (GLU) v[r] = silu(v[r]) * i8_scaled(s[NA - 1][r], st, a.su[nr]);
+  }
+  if (SRC == kNorm) {
+    float m = 0.f;
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (n + r < N) m = fmaxf(m, fabsf(v[r]));
+    m = fmaxf(m, __shfl_xor(m, 16));
+    m = fmaxf(m, __shfl_xor(m, 32));
+    if (q == 0 && t < T) a.hmax[int64_t(t) * gridDim.x + blockIdx.x] = m;
+  }
+  if (t < T)
+    store_out4<TO>(static_cast<TO*>(a.y), static_cast<const TO*>(a.res), int64_t(t) * N, n, N, a.vec, v);
 }
 
 // 16-byte chunks of the tile's LDS rows are XOR-swizzled so that the 16 consecutive rows one
@@ -164,9 +348,11 @@ __device__ __forceinline__ bool i8_tile_item(int mtiles, int ntiles, int& mt, in
 // consecutive columns of a token, so that stores are 16 bytes and contiguous over the lanes.
 template <typename TO, bool GLU, class C>
 __device__ __forceinline__ void i8_epilogue(unsigned char* stg, const i32x4 (&acc)[C::FN][C::FM],
-                                            const float* sx, const float* sw, const float* su,
-                                            const TO* res, TO* y, int64_t T, int N, int64_t tw,
-                                            int nw, bool vec, int lane) {
+                                            const I8Args& a, int64_t tw, int nw, int lane) {
+  const int64_t T = a.T;
+  const int N = a.N;
+  const TO* const res = static_cast<const TO*>(a.res);
+  TO* const y = static_cast<TO*>(a.y);
   constexpr int RS = C::TN + 4;                       // ints per staged row
   constexpr int OC = GLU ? C::TN / 2 : C::TN;
   constexpr int LPR = OC / 8, RPP = 64 / LPR;         // lanes per row, rows per pass
@@ -175,8 +361,8 @@ __device__ __forceinline__ void i8_epilogue(unsigned char* stg, const i32x4 (&ac
   float s0[8], s1[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    s0[i] = sw[min(n + i, N - 1)];
-    s1[i] = GLU ? su[min(n + i, N - 1)] : 0.f;
+    s0[i] = a.sw[min(n + i, N - 1)];
+    s1[i] = GLU ? a.su[min(n + i, N - 1)] : 0.f;
   }
 #pragma unroll
   for (int m = 0; m < C::FM / 2; ++m) {
@@ -192,7 +378,7 @@ __device__ __forceinline__ void i8_epilogue(unsigned char* stg, const i32x4 (&ac
       const int64_t t = tw + m * 32 + row;
       const i32x4 a0 = *reinterpret_cast<const i32x4*>(st + row * RS + c8);
       const i32x4 a1 = *reinterpret_cast<const i32x4*>(st + row * RS + c8 + 4);
-      const float ts = sx[min<int64_t>(t, T - 1)];
+      const float ts = a.sx[min<int64_t>(t, T - 1)];
       float v[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = i8_scaled(i < 4 ? a0[i & 3] : a1[i & 3], ts, s0[i]);
@@ -205,7 +391,7 @@ __device__ __forceinline__ void i8_epilogue(unsigned char* stg, const i32x4 (&ac
       }
       if (t >= T || n >= N) continue;
       const int64_t at = t * N + n;
-      if (vec) {
+      if (a.vec) {
         if (res) {
           float r[8];
           load8(res + at, r);
@@ -263,21 +449,16 @@ __device__ __forceinline__ void i8_slab_sync() {
 // read during the phase before.
 // 8192 x 4096 x 8192: 233 us, 2.35e15 op/s; 8192 x 8192 x 2048: 111 us, 2.47e15.
 template <typename TO, bool GLU, class C>
-__global__ __launch_bounds__(C::NW * 64) void k_i8_tile(const int8_t* __restrict__ x,
-                                                        const float* __restrict__ sx,
-                                                        const int8_t* __restrict__ w,
-                                                        const float* __restrict__ sw,
-                                                        const int8_t* __restrict__ wu,
-                                                        const float* __restrict__ su,
-                                                        const TO* res, TO* y, int64_t T, int K,
-                                                        int N, int mtiles, int ntiles, bool vec) {
+__global__ __launch_bounds__(C::NW * 64) void k_i8_tile(I8Args a) {
   constexpr int OC = GLU ? C::TN / 2 : C::TN;              // output columns per wave
   __shared__ __align__(16) unsigned char lds[C::LDS];
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
   const int pos = wv % C::NP, kw = wv / C::NP;
   const int wm = pos / C::NWN, wn = pos % C::NWN;
   int mt, nt;
-  if (!i8_tile_item(mtiles, ntiles, mt, nt)) return;
+  if (!i8_tile_item(a.mtiles, a.ntiles, mt, nt)) return;
+  const int64_t T = a.T;
+  const int K = a.K, N = a.N;
   const int64_t t0 = int64_t(mt) * C::BM;
   const int n0 = nt * (GLU ? C::BN / 2 : C::BN);
 
@@ -289,15 +470,15 @@ __global__ __launch_bounds__(C::NW * 64) void k_i8_tile(const int8_t* __restrict
     const int r = (wv + C::NW * i) * (64 / C::CPR) + lane / C::CPR;
     kc[i] = ((lane % C::CPR) ^ i8_swz<C::BK>(r)) * 16;
     if (r < C::BM) {
-      src[i] = x + min<int64_t>(t0 + r, T - 1) * K;
+      src[i] = a.x + min<int64_t>(t0 + r, T - 1) * K;
     } else {
       const int q = r - C::BM;
       if (GLU) {
         const int s = q % C::TN;
         const int n = min(n0 + q / C::TN * OC + s % OC, N - 1);
-        src[i] = (s < OC ? w : wu) + int64_t(n) * K;
+        src[i] = (s < OC ? a.w : a.wu) + int64_t(n) * K;
       } else {
-        src[i] = w + int64_t(min(n0 + q, N - 1)) * K;
+        src[i] = a.w + int64_t(min(n0 + q, N - 1)) * K;
       }
     }
   }
@@ -409,24 +590,32 @@ __global__ __launch_bounds__(C::NW * 64) void k_i8_tile(const int8_t* __restrict
     __syncthreads();
     if (kw > 0) return;
   }
-  i8_epilogue<TO, GLU, C>(lds + pos * C::STG, acc, sx, sw, su, res, y, T, N, t0 + wm * C::TM,
-                          n0 + wn * OC, vec, lane);
+  i8_epilogue<TO, GLU, C>(lds + pos * C::STG, acc, a, t0 + wm * C::TM, n0 + wn * OC, lane);
+}
+
+static I8Args i8_args(const I8Product& p) {
+  auto aligned = [](const void* q) { return (reinterpret_cast<uintptr_t>(q) & 15) == 0; };
+  I8Args a{};
+  a.x = p.x; a.sx = p.sx; a.w = p.w; a.sw = p.sw; a.wu = p.w_up; a.su = p.s_up;
+  a.res = p.res; a.y = p.y; a.T = p.T; a.K = p.K; a.N = p.N;
+  a.vec = p.N % 8 == 0 && aligned(p.y) && (!p.res || aligned(p.res));
+  return a;
 }
 
 template <typename TO, bool GLU, int TB>
-static void launch_few(const I8Product& p, bool vec, hipStream_t st) {
-  hipLaunchKernelGGL((k_i8_few<TO, TB, GLU>), dim3(unsigned((p.N + 15) / 16)), dim3(512), 0, st, p.x,
-                     p.sx, p.w, p.sw, p.w_up, p.s_up, static_cast<const TO*>(p.res),
-                     static_cast<TO*>(p.y), p.T, p.K, p.N, vec);
+static void launch_few(const I8Product& p, hipStream_t st) {
+  hipLaunchKernelGGL((k_i8_few<TO, TB, GLU, kCodes, FewNone>), dim3(unsigned((p.N + 15) / 16)),
+                     dim3(512), 0, st, i8_args(p));
 }
 
 template <typename TO, bool GLU, class C>
-static void launch_tile(const I8Product& p, bool vec, hipStream_t st) {
+static void launch_tile(const I8Product& p, hipStream_t st) {
   const int64_t mt = (p.T + C::BM - 1) / C::BM, oc = GLU ? C::BN / 2 : C::BN;
   const int64_t nt = (p.N + oc - 1) / oc;
-  hipLaunchKernelGGL((k_i8_tile<TO, GLU, C>), dim3(xcd_grid(mt * nt)), dim3(C::NW * 64), 0, st, p.x,
-                     p.sx, p.w, p.sw, p.w_up, p.s_up, static_cast<const TO*>(p.res),
-                     static_cast<TO*>(p.y), p.T, p.K, p.N, int(mt), int(nt), vec);
+  I8Args a = i8_args(p);
+  a.mtiles = int(mt);
+  a.ntiles = int(nt);
+  hipLaunchKernelGGL((k_i8_tile<TO, GLU, C>), dim3(xcd_grid(mt * nt)), dim3(C::NW * 64), 0, st, a);
 }
 
 // The tiles: one workgroup of the largest per CU, two or three of the smaller ones.
@@ -445,14 +634,14 @@ using Tile32 = I8Tile<32, 64, 1, 2, 256, 2, 4>;
 // 2048 32x64 7.6, 64x64 7.3, 128x128 13.9; 2048 x 2048 x 2048 64x64 19.5, 128x128 16.5;
 // 8192 x 8192 x 2048 128x128 152, 256x256 111.
 template <typename TO, bool GLU>
-static int launch_product(const I8Product& p, bool vec, hipStream_t st) {
+static int launch_product(const I8Product& p, hipStream_t st) {
   if (p.T <= 16) {
-    launch_few<TO, GLU, 1>(p, vec, st);
+    launch_few<TO, GLU, 1>(p, st);
     return check_launch();
   }
   if constexpr (!GLU) {
     if (p.T <= 32) {
-      launch_few<TO, GLU, 2>(p, vec, st);
+      launch_few<TO, GLU, 2>(p, st);
       return check_launch();
     }
   }
@@ -466,22 +655,53 @@ static int launch_product(const I8Product& p, bool vec, hipStream_t st) {
   const double e64 = std::max(1.0, tiles(64, 64)) * slabs * 0.22 + 4.2;
   const double e32 = std::max(1.0, tiles(32, 64)) * slabs * 0.14 + 3.4;
   if (e256 <= std::min(e128, std::min(e64, e32)))
-    launch_tile<TO, GLU, Tile256>(p, vec, st);
+    launch_tile<TO, GLU, Tile256>(p, st);
   else if (e128 <= std::min(e64, e32))
-    launch_tile<TO, GLU, Tile128>(p, vec, st);
+    launch_tile<TO, GLU, Tile128>(p, st);
   else if (e64 <= e32)
-    launch_tile<TO, GLU, Tile64>(p, vec, st);
+    launch_tile<TO, GLU, Tile64>(p, st);
   else
-    launch_tile<TO, GLU, Tile32>(p, vec, st);
+    launch_tile<TO, GLU, Tile32>(p, st);
   return check_launch();
 }
 
 int launch_i8_product(const I8Product& p, hipStream_t st) {
-  auto aligned = [](const void* a) { return (reinterpret_cast<uintptr_t>(a) & 15) == 0; };
-  const bool vec = p.N % 8 == 0 && aligned(p.y) && (!p.res || aligned(p.res));
   if (p.out == MOE_F32)
-    return p.w_up ? launch_product<float, true>(p, vec, st) : launch_product<float, false>(p, vec, st);
-  return p.w_up ? launch_product<bf16_t, true>(p, vec, st) : launch_product<bf16_t, false>(p, vec, st);
+    return p.w_up ? launch_product<float, true>(p, st) : launch_product<float, false>(p, st);
+  return p.w_up ? launch_product<bf16_t, true>(p, st) : launch_product<bf16_t, false>(p, st);
+}
+
+// The dense layer of up to 16 tokens in two launches: norm, codes and gated product; codes of
+// h, down product and residual.  Every workgroup makes the codes it needs (a few rows, from L2)
+// while its first weights are on their way, which costs less than a launch between the stages.
+bool dense_few_ok(int64_t T, int H, int I) {
+  return T <= 16 && H <= 4096 && T * few_stride(H) <= kFewCodes && T * few_stride(I) <= kFewCodes;
+}
+size_t dense_few_hmax_bytes(int64_t T, int I) { return size_t(T) * ((I + 15) / 16) * sizeof(float); }
+
+template <typename TA>
+static int launch_dense_few_act(const DenseFew& d, hipStream_t st) {
+  I8Args up{};
+  up.w = d.w->w_gate; up.sw = d.w->s_gate; up.wu = d.w->w_up; up.su = d.w->s_up;
+  up.y = d.h; up.T = d.T; up.K = d.H; up.N = d.I; up.vec = d.I % 8 == 0;
+  up.rows = d.x; up.gamma = d.gamma; up.eps = d.eps; up.hmax = d.hmax;
+  const dim3 gu(unsigned((d.I + 15) / 16)), gd(unsigned((d.H + 15) / 16));
+  const size_t lu = size_t(d.T) * few_stride(d.H), ld = size_t(d.T) * few_stride(d.I);
+  if (d.H <= 2048)
+    hipLaunchKernelGGL((k_i8_few<float, 1, true, kNorm, FewNorm<TA, 4>>), gu, dim3(512), lu, st, up);
+  else
+    hipLaunchKernelGGL((k_i8_few<float, 1, true, kNorm, FewNorm<TA, 8>>), gu, dim3(512), lu, st, up);
+  MOE_TRY(check_launch());
+  I8Args down{};
+  down.w = d.w->w_down; down.sw = d.w->s_down; down.res = d.x; down.y = d.x_out;
+  down.T = d.T; down.K = d.I; down.N = d.H; down.vec = d.H % 8 == 0;
+  down.rows = d.h; down.hmax = d.hmax;
+  hipLaunchKernelGGL((k_i8_few<TA, 1, false, kQuant, FewQuant>), gd, dim3(512), ld, st, down);
+  return check_launch();
+}
+
+int launch_dense_few(const DenseFew& d, hipStream_t st) {
+  return d.act == MOE_F32 ? launch_dense_few_act<float>(d, st) : launch_dense_few_act<bf16_t>(d, st);
 }
 
 }  // namespace moe

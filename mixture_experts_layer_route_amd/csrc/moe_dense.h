@@ -41,6 +41,22 @@ struct I8Product {
 };
 int launch_i8_product(const I8Product& p, hipStream_t st);
 
+// The dense layer of a few tokens in two launches
+struct DenseFew {
+  int64_t T;
+  int H, I, act;
+  const void* x;
+  const void* gamma;
+  float eps;
+  const moe_dense_weights* w;
+  float* h;                // [T, I]
+  float* hmax;             // dense_few_hmax_bytes()
+  void* x_out;
+};
+bool dense_few_ok(int64_t T, int H, int I);
+size_t dense_few_hmax_bytes(int64_t T, int I);
+int launch_dense_few(const DenseFew& d, hipStream_t st);
+
 #ifdef __HIPCC__
 // Per-row int8: scale = amax / 127.  A row whose amax is so small that the scale would leave
 // the normal floats (or is zero) has scale 1 and codes 0, so no division overflows.

@@ -21,9 +21,15 @@ namespace moe {
 // x, res and x_sum may be the same memory (a lane stores only chunks it has loaded itself).
 // grid = ceil(T / (4 / WPR)) blocks of 256 threads, or T blocks of 1024 for WPR = 16.
 template <typename TA, int FMT, int WPR, int NCH>
-__global__ __launch_bounds__(WPR == 16 ? 1024 : 256) void k_norm_quant(
-    const TA* x, const TA* res, const TA* __restrict__ gamma, float eps, TA* x_sum, void* out,
-    void* scales, int64_t T, int H) {
+__global__ __launch_bounds__(WPR == 16 ? 1024 : 256) void k_norm_quant(NormQuant a) {
+  const TA* const x = static_cast<const TA*>(a.x);
+  const TA* const res = static_cast<const TA*>(a.res);
+  const TA* const gamma = static_cast<const TA*>(a.gamma);
+  TA* const x_sum = static_cast<TA*>(a.x_sum);
+  void* const out = a.out;
+  void* const scales = a.scales;
+  const int64_t T = a.rows;
+  const int H = a.width;
   constexpr int NW = WPR == 16 ? 16 : 4;         // waves per workgroup
   constexpr int RPB = NW / WPR;                  // rows per workgroup
   __shared__ float part[WPR == 1 ? 1 : 2 * NW];
@@ -76,7 +82,7 @@ __global__ __launch_bounds__(WPR == 16 ? 1024 : 256) void k_norm_quant(
       for (int i = 0; i < WPR; ++i) ss += part[wv / WPR * WPR + i];
     }
     // once per row, in 64 bits: an error here would shift every code of the row
-    const float rinv = float(1.0 / sqrt(double(ss) / H + double(eps)));
+    const float rinv = float(1.0 / sqrt(double(ss) / H + double(a.eps)));
 #pragma unroll
     for (int j = 0; j < NCH; ++j) {
       const int c = j * 64 * WPR + pos;
@@ -149,9 +155,7 @@ static void launch_fmt(const NormQuant& q, hipStream_t st) {
   auto go = [&](auto kern, int wpr) {
     const int rpb = wpr == 1 ? 4 : 1;
     hipLaunchKernelGGL(kern, dim3(unsigned((q.rows + rpb - 1) / rpb)), dim3(wpr == 16 ? 1024 : 256),
-                       0, st, static_cast<const TA*>(q.x), static_cast<const TA*>(q.res),
-                       static_cast<const TA*>(q.gamma), q.eps, static_cast<TA*>(q.x_sum), q.out,
-                       q.scales, q.rows, q.width);
+                       0, st, q);
   };
   // a wave per row needs 4 rows per workgroup and ~8 waves per CU to fill the chip
   const bool batch = q.rows >= 2048;

@@ -127,7 +127,7 @@ def test_dense_layer_refuses(lib):
         lib.moe_dense_residual_i8(c, x, g, eps, ctypes.byref(w) if w is not None else None, o, ws, b, None)
     assert run(x=None) == run(g=None) == run(o=None) == run(ws=None) == run(w=None) == run(c=None) == -1
     assert run(eps=-1.0) == run(eps=float("nan")) == run(ws=FAKE + 16) == -1
-    assert run(x=FAKE + 8) == run(g=FAKE + 8) == run(o=FAKE + 1) == -1
+    assert run(x=FAKE + 8) == run(g=FAKE + 8) == run(o=FAKE + 1) == run(o=FAKE + 8) == -1
     assert run(b=n.value - 1) == -3
     for i in range(6):
         assert run(w=moe.DenseWeights(*[None if j == i else FAKE for j in range(6)])) == -1, i
