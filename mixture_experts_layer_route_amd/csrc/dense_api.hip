@@ -50,6 +50,7 @@ struct DensePlan {
   int64_t T;
   int H, I, act;
   bool few;                // up to 16 tokens: codes never leave the kernels
+  bool h16;                // wide batches: h as int16 codes with group maxima, else fp32
   size_t o_xq, o_sx, o_h, o_hq, o_sh, o_hmax, total;
 };
 
@@ -70,10 +71,13 @@ static int make_dense_plan(const moe_dense_config* c, DensePlan* out) {
   q.few = dense_few_ok(q.T, q.H, q.I);
   q.o_xq = take(q.few ? 0 : size_t(q.T) * q.H);
   q.o_sx = take(q.few ? 0 : size_t(q.T) * 4);
-  q.o_h = take(size_t(q.T) * q.I * 4);   // fp32: h is rounded once, to its codes
+  q.h16 = !q.few && glu_h16_ok(q.T, q.H, q.I);
+  q.o_h = take(size_t(q.T) * q.I * (q.h16 ? 2 : 4));
   q.o_hq = take(q.few ? 0 : size_t(q.T) * q.I);
   q.o_sh = take(q.few ? 0 : size_t(q.T) * 4);
-  q.o_hmax = take(q.few ? dense_few_hmax_bytes(q.T, q.I) : 0);
+  q.o_hmax = take(q.few   ? dense_few_hmax_bytes(q.T, q.I)
+                  : q.h16 ? size_t(q.T) * ((q.I + 31) / 32) * 4
+                          : 0);
   q.total = o;
   *out = q;
   return MOE_OK;
@@ -139,14 +143,20 @@ int moe_dense_residual_i8(const moe_dense_config* cfg, const void* x, const void
   MOE_TRY(check_product(up, true));
   MOE_TRY(check_norm_quant(nh));
   MOE_TRY(check_product(down, false));
+  float* hmax = reinterpret_cast<float*>(base + q.o_hmax);
   if (q.few) {
     const DenseFew d{q.T, q.H, q.I, q.act, x, norm_weight, norm_eps, w, static_cast<float*>(h),
-                     reinterpret_cast<float*>(base + q.o_hmax), x_out};
+                     hmax, x_out};
     return launch_dense_few(d, stream);
   }
   MOE_TRY(launch_norm_quant(nx, stream));
-  MOE_TRY(launch_i8_product(up, stream));
-  MOE_TRY(launch_norm_quant(nh, stream));
+  if (q.h16) {
+    MOE_TRY(launch_glu_h16(up, hmax, stream));
+    MOE_TRY(launch_h16_codes(h, hmax, q.T, q.I, hq, sh, stream));
+  } else {
+    MOE_TRY(launch_i8_product(up, stream));
+    MOE_TRY(launch_norm_quant(nh, stream));
+  }
   return launch_i8_product(down, stream);
 }
 

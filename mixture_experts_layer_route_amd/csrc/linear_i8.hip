@@ -55,8 +55,15 @@ struct I8Args {
   const void* rows;        // kNorm: [T, K] activation rows; kQuant: h, fp32 [T, K]
   const void* gamma;       // kNorm: [K]
   float eps;
-  float* hmax;             // [T, tiles of 16 columns]: largest |h| of a tile, out (kNorm) or in (kQuant)
+  float* hmax;             // [T, groups of columns]: largest |h| of a group, out (kNorm: of 16;
+                           // h16_t: of 32) or in (kQuant: of 16)
 };
+
+// Output of a gated product that goes on to be quantised: int16 codes with one fp32 maximum per
+// row and 32 columns, h = code * max / 32767.  Half the bytes of fp32, and an error of at most
+// 0.5 / 32767 of the group's maximum, 0.002 of a step of the int8 codes made from it (h in bf16
+// moved 3% of those codes).
+struct h16_t { int16_t code; };
 
 // Where a few-row kernel's token codes come from: memory; or made by every workgroup for
 // itself in LDS, from activation rows (RMSNorm in front) or from the fp32 h of the gated product.
@@ -118,10 +125,11 @@ struct FewNorm {
         }
       const float scale = i8_scale(wave_max(m));
       if (lane == 0) sx[t] = scale;
+      const Divider by(scale);
 #pragma unroll
       for (int j = 0; j < NCH; ++j) {
         const int c = j * 64 + lane;
-        if (c < a.K / 8) *reinterpret_cast<uint2*>(codes + t * few_stride(a.K) + c * 8) = i8x8(v[j], scale);
+        if (c < a.K / 8) *reinterpret_cast<uint2*>(codes + t * few_stride(a.K) + c * 8) = i8x8(v[j], by);
       }
     }
   }
@@ -165,18 +173,19 @@ struct FewQuant {
       for (int c = HM * 64 + lane; c < nt; c += 64) m = fmaxf(m, a.hmax[int64_t(t) * nt + c]);
       const float scale = i8_scale(wave_max(m));
       if (lane == 0) sx[t] = scale;          // (the waves of a row write the same value)
+      const Divider by(scale);
       int8_t* const row = codes + t * few_stride(a.K);
 #pragma unroll
       for (int j = 0; j < PRE; ++j) {
         const int c = j * 64 * wpr + (wv % wpr) * 64 + lane;
         float v[8];
         h[i][j].get(v);
-        if (c < a.K / 8) *reinterpret_cast<uint2*>(row + c * 8) = i8x8(v, scale);
+        if (c < a.K / 8) *reinterpret_cast<uint2*>(row + c * 8) = i8x8(v, by);
       }
       for (int c = PRE * 64 * wpr + (wv % wpr) * 64 + lane; c < a.K / 8; c += 64 * wpr) {
         float v[8];
         load8(static_cast<const float*>(a.rows) + int64_t(t) * a.K + c * 8, v);
-        *reinterpret_cast<uint2*>(row + c * 8) = i8x8(v, scale);
+        *reinterpret_cast<uint2*>(row + c * 8) = i8x8(v, by);
       }
     }
   }
@@ -351,8 +360,6 @@ __device__ __forceinline__ void i8_epilogue(unsigned char* stg, const i32x4 (&ac
                                             const I8Args& a, int64_t tw, int nw, int lane) {
   const int64_t T = a.T;
   const int N = a.N;
-  const TO* const res = static_cast<const TO*>(a.res);
-  TO* const y = static_cast<TO*>(a.y);
   constexpr int RS = C::TN + 4;                       // ints per staged row
   constexpr int OC = GLU ? C::TN / 2 : C::TN;
   constexpr int LPR = OC / 8, RPP = 64 / LPR;         // lanes per row, rows per pass
@@ -386,9 +393,31 @@ __device__ __forceinline__ void i8_epilogue(unsigned char* stg, const i32x4 (&ac
         const i32x4 b0 = *reinterpret_cast<const i32x4*>(st + row * RS + OC + c8);
         const i32x4 b1 = *reinterpret_cast<const i32x4*>(st + row * RS + OC + c8 + 4);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          v[i] = silu(v[i]) * i8_scaled(i < 4 ? b0[i & 3] : b1[i & 3], ts, s1[i]);
+        for (int i = 0; i < 8; ++i) {
+          const float u = i8_scaled(i < 4 ? b0[i & 3] : b1[i & 3], ts, s1[i]);
+          v[i] = (sizeof(TO) == 4 ? silu(v[i]) : silu16(v[i])) * u;
+        }
       }
+      if constexpr (std::is_same<TO, h16_t>::value) {
+        // a wave's 32 columns are one group, four lanes of a quad hold a row of it
+        static_assert(GLU && OC == 32, "groups of 32 columns");
+        float m = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = fmaxf(m, n < N ? fabsf(v[i]) : 0.f);
+        m = fmaxf(m, dppf<0xB1>(m));    // quad_perm [1,0,3,2]
+        m = fmaxf(m, dppf<0x4E>(m));    // quad_perm [2,3,0,1]
+        if (t >= T || n >= N) continue;
+        const float up = m >= 1.17549435e-38f ? 32767.0f / m : 0.0f;
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          w[i] = (uint32_t(int(rintf(v[2 * i] * up))) & 0xFFFFu) | (uint32_t(int(rintf(v[2 * i + 1] * up))) << 16);
+        *reinterpret_cast<uint4*>(static_cast<int16_t*>(a.y) + t * N + n) = make_uint4(w[0], w[1], w[2], w[3]);
+        if (lane % LPR == 0) a.hmax[t * ((N + 31) / 32) + n / 32] = m;
+        continue;
+      } else {
+      const TO* const res = static_cast<const TO*>(a.res);
+      TO* const y = static_cast<TO*>(a.y);
       if (t >= T || n >= N) continue;
       const int64_t at = t * N + n;
       if (a.vec) {
@@ -403,6 +432,7 @@ __device__ __forceinline__ void i8_epilogue(unsigned char* stg, const i32x4 (&ac
 #pragma unroll
         for (int i = 0; i < 8; ++i)
           if (n + i < N) y[at + i] = from_f32<TO>(res ? v[i] + to_f32<TO>(res[at + i]) : v[i]);
+      }
       }
     }
   }
@@ -609,12 +639,13 @@ static void launch_few(const I8Product& p, hipStream_t st) {
 }
 
 template <typename TO, bool GLU, class C>
-static void launch_tile(const I8Product& p, hipStream_t st) {
+static void launch_tile(const I8Product& p, hipStream_t st, float* hmax = nullptr) {
   const int64_t mt = (p.T + C::BM - 1) / C::BM, oc = GLU ? C::BN / 2 : C::BN;
   const int64_t nt = (p.N + oc - 1) / oc;
   I8Args a = i8_args(p);
   a.mtiles = int(mt);
   a.ntiles = int(nt);
+  a.hmax = hmax;
   hipLaunchKernelGGL((k_i8_tile<TO, GLU, C>), dim3(xcd_grid(mt * nt)), dim3(C::NW * 64), 0, st, a);
 }
 
@@ -627,41 +658,101 @@ using Tile32 = I8Tile<32, 64, 1, 2, 256, 2, 4>;
 // Which kernel: up to 16 tokens (32 without the gate) the weights are streamed past every
 // token at once; beyond, the tile whose estimated time is least.  The estimate is
 //   (tiles per CU) * (128-wide K slabs) * (time per slab and tile) + (start and end),
-// fitted to measurements from 64 to 8192 tokens (us: slab 0.14 / 0.22 / 0.6 / 1.63, start
+// fitted to measurements from 64 to 8192 tokens (us: slab 0.14 / 0.24 / 0.6 / 1.63, start
 // and end 3.4 / 4.2 / 5 / 6 for 32x64, 64x64, 128x128, 256x256).  The smaller tiles share a CU,
 // so a part of a round costs a part of it; the largest pays whole rounds, ends included.
 // Measured on either side of a switch (us): 64 x 1536 x 4096 few 5.9, 32x64 5.1; 512 x 2048 x
 // 2048 32x64 7.6, 64x64 7.3, 128x128 13.9; 2048 x 2048 x 2048 64x64 19.5, 128x128 16.5;
 // 8192 x 8192 x 2048 128x128 152, 256x256 111.
-template <typename TO, bool GLU>
-static int launch_product(const I8Product& p, hipStream_t st) {
-  if (p.T <= 16) {
-    launch_few<TO, GLU, 1>(p, st);
-    return check_launch();
-  }
-  if constexpr (!GLU) {
-    if (p.T <= 32) {
-      launch_few<TO, GLU, 2>(p, st);
-      return check_launch();
-    }
-  }
-  const double slabs = double((p.K + 127) / 128);
+enum I8Kernel { kFew16, kFew32, kTile32, kTile64, kTile128, kTile256 };
+static I8Kernel pick_kernel(int64_t T, int K, int N, bool glu) {
+  if (T <= 16) return kFew16;
+  if (T <= 32 && !glu) return kFew32;
+  const double slabs = double((K + 127) / 128);
   auto tiles = [&](int bm, int bn) {
-    const int oc = GLU ? bn / 2 : bn;
-    return double((p.T + bm - 1) / bm) * double((p.N + oc - 1) / oc) / 256.0;
+    const int oc = glu ? bn / 2 : bn;
+    return double((T + bm - 1) / bm) * double((N + oc - 1) / oc) / 256.0;
   };
   const double e256 = std::ceil(tiles(256, 256)) * (slabs * 1.63 + 6.0);
   const double e128 = std::max(1.0, tiles(128, 128)) * slabs * 0.6 + 5.0;
-  const double e64 = std::max(1.0, tiles(64, 64)) * slabs * 0.22 + 4.2;
+  const double e64 = std::max(1.0, tiles(64, 64)) * slabs * 0.24 + 4.2;
   const double e32 = std::max(1.0, tiles(32, 64)) * slabs * 0.14 + 3.4;
-  if (e256 <= std::min(e128, std::min(e64, e32)))
-    launch_tile<TO, GLU, Tile256>(p, st);
-  else if (e128 <= std::min(e64, e32))
-    launch_tile<TO, GLU, Tile128>(p, st);
-  else if (e64 <= e32)
-    launch_tile<TO, GLU, Tile64>(p, st);
-  else
-    launch_tile<TO, GLU, Tile32>(p, st);
+  if (e256 <= std::min(e128, std::min(e64, e32))) return kTile256;
+  if (e128 <= std::min(e64, e32)) return kTile128;
+  return e64 <= e32 ? kTile64 : kTile32;
+}
+bool glu_h16_ok(int64_t T, int K, int N) { return pick_kernel(T, K, N, true) == kTile256; }
+
+template <typename TO, bool GLU>
+static int launch_product(const I8Product& p, hipStream_t st) {
+  switch (pick_kernel(p.T, p.K, p.N, GLU)) {
+    case kFew16: launch_few<TO, GLU, 1>(p, st); break;
+    case kFew32:
+      if constexpr (!GLU) launch_few<TO, GLU, 2>(p, st);
+      break;
+    case kTile32: launch_tile<TO, GLU, Tile32>(p, st); break;
+    case kTile64: launch_tile<TO, GLU, Tile64>(p, st); break;
+    case kTile128: launch_tile<TO, GLU, Tile128>(p, st); break;
+    case kTile256: launch_tile<TO, GLU, Tile256>(p, st); break;
+  }
+  return check_launch();
+}
+
+int launch_glu_h16(const I8Product& p, float* hmax, hipStream_t st) {
+  launch_tile<h16_t, true, Tile256>(p, st, hmax);
+  return check_launch();
+}
+
+// int8 codes and scales of rows of h held as h16_t; a workgroup per row, every value read once
+// (the row's maximum comes from its groups').  grid = T, block = 256.
+__global__ __launch_bounds__(256) void k_h16_codes(const int16_t* h, const float* hmax, int I,
+                                                   int8_t* codes, float* scales) {
+  constexpr int PRE = 4;
+  __shared__ float part[4];
+  const int64_t t = blockIdx.x;
+  const int tid = threadIdx.x, n8 = I / 8, ng = (I + 31) / 32;
+  const int16_t* const row = h + t * I;
+  const float* const gm = hmax + t * ng;
+  uint4 c[PRE];
+  float m32[PRE];
+#pragma unroll
+  for (int j = 0; j < PRE; ++j) {
+    const int k = min(j * 256 + tid, n8 - 1);
+    c[j] = *reinterpret_cast<const uint4*>(row + k * 8);
+    m32[j] = gm[k / 4];
+  }
+  float m = 0.f;
+  for (int g = tid; g < ng; g += 256) m = fmaxf(m, gm[g]);
+  m = wave_max(m);
+  if ((tid & 63) == 0) part[tid >> 6] = m;
+  __syncthreads();
+  m = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
+  const float scale = i8_scale(m);
+  if (tid == 0) scales[t] = scale;
+  const float step = 1.0f / (32767.0f * scale);     // codes of h16 -> codes, times the group's maximum
+  auto put = [&](int k, const uint4& v, float mg) {
+    const float f = mg * step;
+    const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+    uint32_t w[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int x = int(in[i / 2] << (i % 2 ? 0 : 16)) >> 16;
+      const float q = fminf(fmaxf(rintf(float(x) * f), -127.f), 127.f);
+      w[i / 4] |= (uint32_t(int(q)) & 0xFFu) << (8 * (i % 4));
+    }
+    *reinterpret_cast<uint2*>(codes + t * I + k * 8) = make_uint2(w[0], w[1]);
+  };
+#pragma unroll
+  for (int j = 0; j < PRE; ++j)
+    if (j * 256 + tid < n8) put(j * 256 + tid, c[j], m32[j]);
+  for (int k = PRE * 256 + tid; k < n8; k += 256)
+    put(k, *reinterpret_cast<const uint4*>(row + k * 8), gm[k / 4]);
+}
+
+int launch_h16_codes(const void* h, const float* hmax, int64_t T, int I, int8_t* codes, float* scales,
+                     hipStream_t st) {
+  hipLaunchKernelGGL(k_h16_codes, dim3(unsigned(T)), dim3(256), 0, st, static_cast<const int16_t*>(h),
+                     hmax, I, codes, scales);
   return check_launch();
 }
 

@@ -41,6 +41,13 @@ struct I8Product {
 };
 int launch_i8_product(const I8Product& p, hipStream_t st);
 
+// The gated product with h as int16 codes and group maxima ([T, N] and [T, ceil(N / 32)]; out is
+// ignored), where the widest tile is the one chosen; and the int8 codes of such rows.
+bool glu_h16_ok(int64_t T, int K, int N);
+int launch_glu_h16(const I8Product& p, float* hmax, hipStream_t st);
+int launch_h16_codes(const void* h, const float* hmax, int64_t T, int I, int8_t* codes, float* scales,
+                     hipStream_t st);
+
 // The dense layer of a few tokens in two launches
 struct DenseFew {
   int64_t T;
@@ -69,13 +76,29 @@ __device__ __forceinline__ float e4m3_scale(float amax) {
   const float s = amax / 448.0f;
   return s >= 1.17549435e-38f ? s : 1.0f;
 }
+// v / scale for many values of one scale: the product with the reciprocal and one correction
+// step, within an ulp of the quotient, in three operations where the division sequence takes
+// about ten.
+struct Divider {
+  float scale, inv;
+  __device__ __forceinline__ explicit Divider(float s) : scale(s), inv(1.0f / s) {}
+  __device__ __forceinline__ float operator()(float v) const {
+    const float q = v * inv;
+    return fmaf(fmaf(-q, scale, v), inv, q);
+  }
+};
+// SiLU with the hardware reciprocal (an ulp), for outputs of 16 bits.  The denominator is taken at
+// a sixteenth, so that its reciprocal stays a normal float up to where exp(-g) overflows.
+__device__ __forceinline__ float silu16(float g) {
+  return (g * 0.0625f) * __builtin_amdgcn_rcpf(fmaf(__expf(-g), 0.0625f, 0.0625f));
+}
 // Eight values -> eight int8 codes, round to nearest even (|v| / scale <= 127 up to the
 // division's rounding, which the clamp takes back).
-__device__ __forceinline__ uint2 i8x8(const float (&v)[8], float scale) {
+__device__ __forceinline__ uint2 i8x8(const float (&v)[8], const Divider& by) {
   uint32_t w[2] = {0, 0};
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float q = fminf(fmaxf(rintf(v[i] / scale), -127.f), 127.f);
+    const float q = fminf(fmaxf(rintf(by(v[i])), -127.f), 127.f);
     w[i / 4] |= (uint32_t(int(q)) & 0xFFu) << (8 * (i % 4));
   }
   return make_uint2(w[0], w[1]);

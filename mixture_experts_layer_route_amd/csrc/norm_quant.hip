@@ -113,6 +113,7 @@ __global__ __launch_bounds__(WPR == 16 ? 1024 : 256) void k_norm_quant(NormQuant
     row_scale = i8_scale(m);
     if (pos == 0) static_cast<float*>(scales)[t] = row_scale;
   }
+  const Divider row_by(row_scale);
 #pragma unroll
   for (int j = 0; j < NCH; ++j) {
     const int c = j * 64 * WPR + pos;
@@ -122,7 +123,7 @@ __global__ __launch_bounds__(WPR == 16 ? 1024 : 256) void k_norm_quant(NormQuant
       if (live) store8(static_cast<TA*>(out) + off, v[j]);
     } else if (FMT == MOE_ROWS_I8) {
       if (live)
-        *reinterpret_cast<uint2*>(static_cast<int8_t*>(out) + off) = i8x8(v[j], row_scale);
+        *reinterpret_cast<uint2*>(static_cast<int8_t*>(out) + off) = i8x8(v[j], row_by);
     } else {
       float m = 0.f;
 #pragma unroll
@@ -134,8 +135,9 @@ __global__ __launch_bounds__(WPR == 16 ? 1024 : 256) void k_norm_quant(NormQuant
         m = fmaxf(m, dppf<0x141>(m));   // row_half_mirror
         m = fmaxf(m, dppf<0x140>(m));   // row_mirror
         const float s = e4m3_scale(m);
-        c0 = e4m3x4(v[j][0] / s, v[j][1] / s, v[j][2] / s, v[j][3] / s);
-        c1 = e4m3x4(v[j][4] / s, v[j][5] / s, v[j][6] / s, v[j][7] / s);
+        const Divider by(s);
+        c0 = e4m3x4(by(v[j][0]), by(v[j][1]), by(v[j][2]), by(v[j][3]));
+        c1 = e4m3x4(by(v[j][4]), by(v[j][5]), by(v[j][6]), by(v[j][7]));
         if (live && (lane & 15) == 0) static_cast<float*>(scales)[t * (H / 128) + c / 16] = s;
       } else {
         const int X = mx_exponent(m);

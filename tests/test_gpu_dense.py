@@ -294,7 +294,8 @@ def layer(g, H, I, act):
 @pytest.mark.parametrize("T,H,I,act", [(1, 1536, 5120, "bf16"), (1, 16, 16, "f32"), (2, 272, 400, "bf16"),
                                        (4, 1536, 4112, "f32"), (9, 2048, 1040, "bf16"), (16, 4096, 8192, "bf16"),
                                        (17, 1536, 512, "bf16"), (16, 4112, 272, "bf16"), (64, 1536, 512, "f32"),
-                                       (333, 1536, 4112, "bf16"), (2100, 512, 784, "bf16"), (16, 2048, 32768, "bf16")])
+                                       (333, 1536, 4112, "bf16"), (2100, 512, 784, "bf16"), (16, 2048, 32768, "bf16"),
+                                       (4090, 2048, 8176, "bf16"), (7900, 2048, 4112, "f32")])
 def test_dense_layer(moe, T, H, I, act):
     """x_out against the oracle run through all four stages.
 
