@@ -328,7 +328,7 @@ def _raw_stream(dev: int) -> int:
 
 def _device() -> int:
     """The current device's index (-1 without one: every argument check then fails)."""
-    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -1
+    return torch._C._cuda_getDevice() if torch.cuda._initialized else -1
 
 
 def _arg(name: str, t: torch.Tensor, shape: tuple, dtype: torch.dtype, dev: int) -> int:
@@ -336,7 +336,7 @@ def _arg(name: str, t: torch.Tensor, shape: tuple, dtype: torch.dtype, dev: int)
     device (the library launches on that device and checks nothing behind a pointer).  A call
     makes up to seven of these checks beside a launch of a few microseconds, so they use the
     cheapest accessors there are (get_device() of a host tensor is -1)."""
-    if t.dtype != dtype or t.shape != shape:
+    if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{name}: expected {dtype} {shape}, got {t.dtype} {tuple(t.shape)}")
     if t.get_device() != dev or dev < 0:
         raise ValueError(f"{name}: expected a tensor on the current device, got {t.device}")
@@ -352,9 +352,10 @@ def _act_dtype(name: str, dtype: torch.dtype) -> int:
 
 
 def _rows_of(name: str, t: torch.Tensor):
-    if t.dim() != 2:
-        raise ValueError(f"{name}: expected [rows, width], got {tuple(t.shape)}")
-    return t.shape
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name}: expected [rows, width], got {tuple(shape)}")
+    return shape
 
 
 def norm_quant_rows(x, fmt: str, norm_weight: Optional[torch.Tensor] = None,
@@ -378,14 +379,18 @@ def norm_quant_rows(x, fmt: str, norm_weight: Optional[torch.Tensor] = None,
     if residual is not None:
         rp = _arg("residual", residual, (T, H), x.dtype, dev)
         if x_sum is None:
-            x_sum = torch.empty_like(x)
-        sp = _arg("x_sum", x_sum, (T, H), x.dtype, dev)
+            x_sum = x.new_empty((T, H))
+            sp = x_sum.data_ptr()
+        else:
+            sp = _arg("x_sum", x_sum, (T, H), x.dtype, dev)
     else:
         x_sum = None
     odt = x.dtype if fmt == "rows" else torch.int8 if fmt == "i8" else torch.uint8
     if out is None:
         out = x.new_empty((T, H), dtype=odt)
-    op = _arg("out", out, (T, H), odt, dev)
+        op = out.data_ptr()
+    else:
+        op = _arg("out", out, (T, H), odt, dev)
     if fmt == "rows":
         scales = None
     else:
@@ -393,7 +398,9 @@ def norm_quant_rows(x, fmt: str, norm_weight: Optional[torch.Tensor] = None,
         sdt = torch.uint8 if fmt == "mxfp8" else torch.float32
         if scales is None:
             scales = x.new_empty(shape, dtype=sdt)
-        cp = _arg("scales", scales, shape, sdt, dev)
+            cp = scales.data_ptr()
+        else:
+            cp = _arg("scales", scales, shape, sdt, dev)
     _check(load_library().moe_norm_quant_rows(T, H, act, ROW_FORMATS[fmt], xp, rp, gp, eps, sp, op,
                                               cp, _raw_stream(dev)))
     return out, scales, x_sum
@@ -415,7 +422,9 @@ def linear_i8(x_codes, x_scales, w_codes, w_scales, out_dtype=torch.bfloat16,
     rp = None if residual is None else _arg("residual", residual, (T, N), out_dtype, dev)
     if y is None:
         y = x_codes.new_empty((T, N), dtype=out_dtype)
-    yp = _arg("y", y, (T, N), out_dtype, dev)
+        yp = y.data_ptr()
+    else:
+        yp = _arg("y", y, (T, N), out_dtype, dev)
     _check(load_library().moe_linear_i8(T, K, N, out, xp, sp, wp, cp, rp, yp, _raw_stream(dev)))
     return y
 
@@ -436,7 +445,9 @@ def glu_i8(x_codes, x_scales, w_gate, s_gate, w_up, s_up, out_dtype=torch.bfloat
     us = _arg("s_up", s_up, (N,), torch.float32, dev)
     if h is None:
         h = x_codes.new_empty((T, N), dtype=out_dtype)
-    hp = _arg("h", h, (T, N), out_dtype, dev)
+        hp = h.data_ptr()
+    else:
+        hp = _arg("h", h, (T, N), out_dtype, dev)
     _check(load_library().moe_glu_i8(T, K, N, out, xp, sp, gp, gs, up, us, hp, _raw_stream(dev)))
     return h
 
@@ -476,8 +487,10 @@ def dense_residual_i8(cfg: DenseConfig, x, norm_weight, wst: DenseWeights, ws,
     xp = _arg("x", x, (T, H), dtype, dev)
     gp = _arg("norm_weight", norm_weight, (H,), dtype, dev)
     if x_out is None:
-        x_out = torch.empty_like(x)
-    op = _arg("x_out", x_out, (T, H), dtype, dev)
+        x_out = x.new_empty((T, H))
+        op = x_out.data_ptr()
+    else:
+        op = _arg("x_out", x_out, (T, H), dtype, dev)
     wp = _arg("ws", ws, (ws.numel(),), torch.uint8, dev)
     _check(load_library().moe_dense_residual_i8(ctypes.byref(cfg), xp, gp, eps, ctypes.byref(wst),
                                                 op, wp, ws.numel(), _raw_stream(dev)))

@@ -357,7 +357,8 @@ __device__ __forceinline__ bool i8_tile_item(int mtiles, int ntiles, int& mt, in
 // consecutive columns of a token, so that stores are 16 bytes and contiguous over the lanes.
 template <typename TO, bool GLU, class C>
 __device__ __forceinline__ void i8_epilogue(unsigned char* stg, const i32x4 (&acc)[C::FN][C::FM],
-                                            const I8Args& a, int64_t tw, int nw, int lane) {
+                                            const I8Args& a, int64_t tw, int nw, int lane,
+                                            const float* sx, const float* sw) {
   const int64_t T = a.T;
   const int N = a.N;
   constexpr int RS = C::TN + 4;                       // ints per staged row
@@ -368,8 +369,8 @@ __device__ __forceinline__ void i8_epilogue(unsigned char* stg, const i32x4 (&ac
   float s0[8], s1[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    s0[i] = a.sw[min(n + i, N - 1)];
-    s1[i] = GLU ? a.su[min(n + i, N - 1)] : 0.f;
+    s0[i] = sw[c8 + i];
+    s1[i] = GLU ? sw[OC + c8 + i] : 0.f;
   }
 #pragma unroll
   for (int m = 0; m < C::FM / 2; ++m) {
@@ -385,7 +386,7 @@ __device__ __forceinline__ void i8_epilogue(unsigned char* stg, const i32x4 (&ac
       const int64_t t = tw + m * 32 + row;
       const i32x4 a0 = *reinterpret_cast<const i32x4*>(st + row * RS + c8);
       const i32x4 a1 = *reinterpret_cast<const i32x4*>(st + row * RS + c8 + 4);
-      const float ts = a.sx[min<int64_t>(t, T - 1)];
+      const float ts = sx[m * 32 + row];
       float v[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = i8_scaled(i < 4 ? a0[i & 3] : a1[i & 3], ts, s0[i]);
@@ -449,15 +450,28 @@ struct I8Tile {
   static constexpr int FM = TM / 16, FN = TN / 16, FH = FM / 2;        // 16x16 blocks of it
   static constexpr int KS = BK / 64 / KW;                              // MFMA steps per slab and wave
   static constexpr int CPR = BK / 16;                                  // 16-byte chunks per row
+  // fragments of two whole slabs fit in registers beside the sums: phases are slabs
+  static constexpr bool WHOLE = 4 * (FM * FN + 2 * KS * (FM + FN)) <= 144;
   static constexpr int SLAB = (BM + BN) * BK;                          // bytes
   static constexpr int L = SLAB / 1024 / NW;                           // loads per lane and slab
   static constexpr int STG = 32 * (TN + 4) * 4;                        // epilogue bytes per wave
   static constexpr int RED = FM * FN * 1024;                           // a wave's sums
   static constexpr int END = NP * (STG > (KW - 1) * RED ? STG : (KW - 1) * RED);
-  static constexpr int LDS = S * SLAB > END ? S * SLAB : END;
+  static constexpr int RING = S * SLAB > END ? S * SLAB : END;
+  static constexpr int LDS = RING + (BM + BN) * 4;                     // + the tile's scales
   static_assert(L * NW * 1024 == SLAB && S >= 2 && FM % 2 == 0 && KS >= 1 && LDS <= 163840,
                 "tile geometry");
 };
+
+// Address of the scale of row r of a tile's slab (tokens first, then weight rows in slab order).
+template <bool GLU, class C>
+__device__ __forceinline__ const float* i8_scale_of(const I8Args& a, int r, int64_t t0, int n0) {
+  constexpr int OC = GLU ? C::TN / 2 : C::TN;
+  if (r < C::BM) return a.sx + min<int64_t>(t0 + r, a.T - 1);
+  const int q = r - C::BM, s = q % C::TN;
+  const int n = min(GLU ? n0 + q / C::TN * OC + s % OC : n0 + q, a.N - 1);
+  return (GLU && s >= OC ? a.su : a.sw) + n;
+}
 
 // All but the N newest loads of this wave have landed and its LDS reads are done, then the
 // workgroup meets.  The fences keep the compiler from moving LDS accesses across either.
@@ -477,7 +491,8 @@ __device__ __forceinline__ void i8_slab_sync() {
 // slot is refilled as soon as the last fragments of it are in registers, half a phase before
 // the slab's end, which is also where the one barrier per slab is; each phase's fragments are
 // read during the phase before.
-// 8192 x 4096 x 8192: 233 us, 2.35e15 op/s; 8192 x 8192 x 2048: 111 us, 2.47e15.
+// 8192 x 4096 x 8192: 226 us, 2.43e15 op/s; 8192 x 8192 x 2048: 111 us, 2.47e15; gated 4096 x
+// 2048 x 8192: 132 us, 2.09e15.
 template <typename TO, bool GLU, class C>
 __global__ __launch_bounds__(C::NW * 64) void k_i8_tile(I8Args a) {
   constexpr int OC = GLU ? C::TN / 2 : C::TN;              // output columns per wave
@@ -512,11 +527,16 @@ __global__ __launch_bounds__(C::NW * 64) void k_i8_tile(I8Args a) {
       }
     }
   }
+  // the tile's scales, tokens then weight rows, by loads older than every slab's
+  float* const scales = reinterpret_cast<float*>(lds + C::RING);
+  static_assert((C::BM + C::BN) % 32 == 0, "whole pieces of scales");
+  for (int i = wv; i < (C::BM + C::BN + 63) / 64; i += C::NW) {
+    const int r = i * 64 + lane;
+    if (r < C::BM + C::BN) dma4(i8_scale_of<GLU, C>(a, r, t0, n0), scales + i * 64);
+  }
   const int nk = (K + C::BK - 1) / C::BK;
-  auto issue = [&](int kt, int slot) {
-#pragma unroll
-    for (int i = 0; i < C::L; ++i)
-      dma16(src[i] + min(kt * C::BK + kc[i], K - 16), lds + slot * C::SLAB + (wv + C::NW * i) * 1024);
+  auto load = [&](int i, int kt, int slot) {
+    dma16(src[i] + min(kt * C::BK + kc[i], K - 16), lds + slot * C::SLAB + (wv + C::NW * i) * 1024);
   };
 
   i32x4 acc[C::FN][C::FM];
@@ -531,71 +551,118 @@ __global__ __launch_bounds__(C::NW * 64) void k_i8_tile(I8Args a) {
   for (int s = 0; s < C::KS; ++s) foff[s] = l16 * C::BK + ((4 * (kw * C::KS + s) + q) ^ i8_swz<C::BK>(l16)) * 16;
   const unsigned char* const xrow = lds + wm * C::TM * C::BK;
   const unsigned char* const wrow = lds + (C::BM + wn * C::TN) * C::BK;
-  i32x4 fx[2][C::FH], fw[2][C::FN];
-  auto read_w = [&](int slot, int s, int buf) {
-#pragma unroll
-    for (int n = 0; n < C::FN; ++n)
-      fw[buf][n] = *reinterpret_cast<const i32x4*>(wrow + slot * C::SLAB + foff[s] + n * 16 * C::BK);
+  auto read_frag = [&](const unsigned char* rows, int slot, int s, int i) {
+    return *reinterpret_cast<const i32x4*>(rows + slot * C::SLAB + foff[s] + i * 16 * C::BK);
   };
-  auto read_x = [&](int slot, int s, int kt, int half) {
-#pragma unroll
-    for (int m = 0; m < C::FH; ++m)
-      fx[half][m] = *reinterpret_cast<const i32x4*>(xrow + slot * C::SLAB + foff[s] +
-                                                    (half * C::FH + m) * 16 * C::BK);
-    if (kt == nk - 1 && kt * C::BK + (4 * (kw * C::KS + s) + q) * 16 >= K) {   // past K: x counts as zero
-#pragma unroll
-      for (int m = 0; m < C::FH; ++m) fx[half][m] = i32x4{0, 0, 0, 0};
-    }
-  };
-  auto mul = [&](int half, int buf) {
-#pragma unroll
-    for (int m = 0; m < C::FH; ++m)
-#pragma unroll
-      for (int n = 0; n < C::FN; ++n)
-        acc[n][half * C::FH + m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(
-            fw[buf][n], fx[half][m], acc[n][half * C::FH + m], 0, 0, 0);
-  };
-
+  // chunks past K hold whatever lies at the clamped address: there x counts as zero
+  auto past = [&](int kt, int s) { return kt * C::BK + (4 * (kw * C::KS + s) + q) * 16 >= K; };
   for (int k = 0; k < C::S; ++k)
-    if (k < nk) issue(k, k);
-  if (nk >= C::S) i8_slab_sync<(C::S - 1) * C::L>(); else i8_slab_sync<0>();
-  read_w(0, 0, 0);
-  read_x(0, 0, 0, 0);
-  int slot = 0;
-  // One slab; WB: buffer its first weight fragments are in.  Every phase multiplies half of
-  // the wave's tokens while the next phase's fragments are read.
-  auto slab = [&](int kt, auto wb) {
-    constexpr int WB = decltype(wb)::value;
-    const int next = slot + 1 == C::S ? 0 : slot + 1;
+    if (k < nk) {
 #pragma unroll
-    for (int s = 0; s < C::KS; ++s) {
-      read_x(slot, s, kt, 1);
-      mul(0, (WB + s) & 1);
-      if (s + 1 < C::KS) {
-        read_w(slot, s + 1, (WB + s + 1) & 1);
-        read_x(slot, s + 1, kt, 0);
-      } else if (kt + 1 < nk) {
-        // every fragment of this slab is in registers: once all waves are here its slot is
-        // free, and slab kt + 1 (older than the S - 2 slabs that may still be on their way)
-        // can be read
-        if (kt + C::S <= nk) i8_slab_sync<(C::S - 2) * C::L>(); else i8_slab_sync<0>();
-        if (kt + C::S < nk) issue(kt + C::S, slot);
-        read_w(next, 0, (WB + s + 1) & 1);
-        read_x(next, 0, kt + 1, 0);
-      }
-      mul(1, (WB + s) & 1);
+      for (int i = 0; i < C::L; ++i) load(i, k, k);
     }
-    slot = next;
-  };
-  if constexpr (C::KS % 2 == 0) {
-    for (int kt = 0; kt < nk; ++kt) slab(kt, std::integral_constant<int, 0>());
-  } else {
+  if (nk >= C::S) i8_slab_sync<(C::S - 1) * C::L>(); else i8_slab_sync<0>();
+  int slot = 0;
+  using Buf0 = std::integral_constant<int, 0>;
+  using Buf1 = std::integral_constant<int, 1>;
+  if constexpr (C::WHOLE) {
+    i32x4 fx[2][C::KS][C::FM], fw[2][C::KS][C::FN];
+    auto read_slab = [&](int sl, int kt, auto buf) {
+      constexpr int B = decltype(buf)::value;
+#pragma unroll
+      for (int s = 0; s < C::KS; ++s) {
+#pragma unroll
+        for (int n = 0; n < C::FN; ++n) fw[B][s][n] = read_frag(wrow, sl, s, n);
+#pragma unroll
+        for (int m = 0; m < C::FM; ++m) fx[B][s][m] = read_frag(xrow, sl, s, m);
+        if (kt == nk - 1 && past(kt, s)) {
+#pragma unroll
+          for (int m = 0; m < C::FM; ++m) fx[B][s][m] = i32x4{0, 0, 0, 0};
+        }
+      }
+    };
+    auto slab = [&](int kt, auto buf, auto other) {
+      constexpr int B = decltype(buf)::value;
+      const int next = slot + 1 == C::S ? 0 : slot + 1;
+      if (kt + 1 < nk) {
+        // this slab is in registers everywhere, so its slot is free, and the next one is in LDS
+        if (kt + C::S <= nk) i8_slab_sync<(C::S - 2) * C::L>(); else i8_slab_sync<0>();
+        if (kt + C::S < nk) {
+#pragma unroll
+          for (int i = 0; i < C::L; ++i) load(i, kt + C::S, slot);
+        }
+        read_slab(next, kt + 1, other);
+      }
+#pragma unroll
+      for (int s = 0; s < C::KS; ++s)
+#pragma unroll
+        for (int m = 0; m < C::FM; ++m)
+#pragma unroll
+          for (int n = 0; n < C::FN; ++n)
+            acc[n][m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fw[B][s][n], fx[B][s][m], acc[n][m], 0, 0, 0);
+      slot = next;
+    };
+    read_slab(0, 0, Buf0());
     int kt = 0;
     for (; kt + 1 < nk; kt += 2) {
-      slab(kt, std::integral_constant<int, 0>());
-      slab(kt + 1, std::integral_constant<int, 1>());
+      slab(kt, Buf0(), Buf1());
+      slab(kt + 1, Buf1(), Buf0());
     }
-    if (kt < nk) slab(kt, std::integral_constant<int, 0>());
+    if (kt < nk) slab(kt, Buf0(), Buf1());
+  } else {
+    static_assert(C::KS % 2 == 0, "a slab starts and ends on the same weight buffer");
+    i32x4 fx[2][C::FH], fw[2][C::FN];
+    auto read_w = [&](int sl, int s, int buf) {
+#pragma unroll
+      for (int n = 0; n < C::FN; ++n) fw[buf][n] = read_frag(wrow, sl, s, n);
+    };
+    auto read_x = [&](int sl, int s, int kt, int half) {
+#pragma unroll
+      for (int m = 0; m < C::FH; ++m) fx[half][m] = read_frag(xrow, sl, s, half * C::FH + m);
+      if (kt == nk - 1 && past(kt, s)) {
+#pragma unroll
+        for (int m = 0; m < C::FH; ++m) fx[half][m] = i32x4{0, 0, 0, 0};
+      }
+    };
+    // half of the wave's tokens; with `lk` >= 0 the loads of slab lk go out between the steps
+    auto mul = [&](int half, int buf, int lk) {
+      constexpr int N = C::FH * C::FN, EVERY = N / C::L;
+      static_assert(EVERY >= 1 && EVERY * C::L == N, "a load every so many steps");
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        const int m = j / C::FN, n = j % C::FN;
+        if (j % EVERY == 0 && lk >= 0) load(j / EVERY, lk, slot);
+        acc[n][half * C::FH + m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(
+            fw[buf][n], fx[half][m], acc[n][half * C::FH + m], 0, 0, 0);
+      }
+    };
+    read_w(0, 0, 0);
+    read_x(0, 0, 0, 0);
+    // Every phase multiplies half of the wave's tokens by one step's weights while the next
+    // phase's fragments are read.
+    for (int kt = 0; kt < nk; ++kt) {
+      const int next = slot + 1 == C::S ? 0 : slot + 1;
+#pragma unroll
+      for (int s = 0; s < C::KS; ++s) {
+        int lk = -1;
+        read_x(slot, s, kt, 1);
+        mul(0, s & 1, -1);
+        if (s + 1 < C::KS) {
+          read_w(slot, s + 1, (s + 1) & 1);
+          read_x(slot, s + 1, kt, 0);
+        } else if (kt + 1 < nk) {
+          // every fragment of this slab is in registers: once all waves are here its slot is
+          // free, and slab kt + 1 (older than the S - 2 slabs that may still be on their way)
+          // can be read
+          if (kt + C::S <= nk) i8_slab_sync<(C::S - 2) * C::L>(); else i8_slab_sync<0>();
+          if (kt + C::S < nk) lk = kt + C::S;
+          read_w(next, 0, 0);
+          read_x(next, 0, kt + 1, 0);
+        }
+        mul(1, s & 1, lk);
+      }
+      slot = next;
+    }
   }
   i8_slab_sync<0>();               // the ring becomes the waves' own staging memory
   if constexpr (C::KW > 1) {
@@ -620,7 +687,8 @@ __global__ __launch_bounds__(C::NW * 64) void k_i8_tile(I8Args a) {
     __syncthreads();
     if (kw > 0) return;
   }
-  i8_epilogue<TO, GLU, C>(lds + pos * C::STG, acc, a, t0 + wm * C::TM, n0 + wn * OC, lane);
+  i8_epilogue<TO, GLU, C>(lds + pos * C::STG, acc, a, t0 + wm * C::TM, n0 + wn * OC, lane,
+                          scales + wm * C::TM, scales + C::BM + wn * C::TN);
 }
 
 static I8Args i8_args(const I8Product& p) {
@@ -651,19 +719,21 @@ static void launch_tile(const I8Product& p, hipStream_t st, float* hmax = nullpt
 
 // The tiles: one workgroup of the largest per CU, two or three of the smaller ones.
 using Tile256 = I8Tile<256, 256, 2, 4, 128, 2>;
-using Tile128 = I8Tile<128, 128, 2, 4, 128, 2>;
-using Tile64 = I8Tile<64, 64, 2, 2, 256, 2, 2>;
-using Tile32 = I8Tile<32, 64, 1, 2, 256, 2, 4>;
+using Tile128 = I8Tile<128, 128, 2, 4, 128, 3>;
+using Tile64 = I8Tile<64, 64, 2, 2, 128, 3, 2>;
+using Tile32 = I8Tile<32, 64, 1, 2, 256, 3, 4>;
 
 // Which kernel: up to 16 tokens (32 without the gate) the weights are streamed past every
 // token at once; beyond, the tile whose estimated time is least.  The estimate is
-//   (tiles per CU) * (128-wide K slabs) * (time per slab and tile) + (start and end),
-// fitted to measurements from 64 to 8192 tokens (us: slab 0.14 / 0.24 / 0.6 / 1.63, start
-// and end 3.4 / 4.2 / 5 / 6 for 32x64, 64x64, 128x128, 256x256).  The smaller tiles share a CU,
-// so a part of a round costs a part of it; the largest pays whole rounds, ends included.
-// Measured on either side of a switch (us): 64 x 1536 x 4096 few 5.9, 32x64 5.1; 512 x 2048 x
-// 2048 32x64 7.6, 64x64 7.3, 128x128 13.9; 2048 x 2048 x 2048 64x64 19.5, 128x128 16.5;
-// 8192 x 8192 x 2048 128x128 152, 256x256 111.
+//   (128-wide K slabs) * max(one slab alone, tiles per CU * a slab among others) + start and end
+// fitted to measurements from 64 to 8192 tokens (us: alone 0.30 / 0.26 / 0.56, among others
+// 0.20 / 0.25 / 0.65, start and end 2.2 / 3.3 / 4 for 32x64, 64x64, 128x128; a round of
+// 256x256 tiles, one per CU, takes 1.65 a slab and 4).  The smaller tiles share a CU, so a part
+// of a round costs a part of it; the largest pays whole rounds.
+// Measured on either side of a switch (us): 64 x 1536 x 4096 few 5.9, 32x64 5.1, 64x64 6.4;
+// 512 x 2048 x 2048 32x64 8.7, 64x64 8.4, 128x128 12.9; 2048 x 2048 x 2048 64x64 19.6, 128x128
+// 15.0; 8192 x 8192 x 2048 128x128 164, 256x256 111; gated 333 x 1536 x 4112 64x64 14.8,
+// 128x128 11.8.
 enum I8Kernel { kFew16, kFew32, kTile32, kTile64, kTile128, kTile256 };
 static I8Kernel pick_kernel(int64_t T, int K, int N, bool glu) {
   if (T <= 16) return kFew16;
@@ -673,10 +743,10 @@ static I8Kernel pick_kernel(int64_t T, int K, int N, bool glu) {
     const int oc = glu ? bn / 2 : bn;
     return double((T + bm - 1) / bm) * double((N + oc - 1) / oc) / 256.0;
   };
-  const double e256 = std::ceil(tiles(256, 256)) * (slabs * 1.63 + 6.0);
-  const double e128 = std::max(1.0, tiles(128, 128)) * slabs * 0.6 + 5.0;
-  const double e64 = std::max(1.0, tiles(64, 64)) * slabs * 0.24 + 4.2;
-  const double e32 = std::max(1.0, tiles(32, 64)) * slabs * 0.14 + 3.4;
+  const double e256 = std::ceil(tiles(256, 256)) * (slabs * 1.65 + 4.0);
+  const double e128 = slabs * std::max(0.56, tiles(128, 128) * 0.65) + 4.0;
+  const double e64 = slabs * std::max(0.26, tiles(64, 64) * 0.25) + 3.3;
+  const double e32 = slabs * std::max(0.30, tiles(32, 64) * 0.20) + 2.2;
   if (e256 <= std::min(e128, std::min(e64, e32))) return kTile256;
   if (e128 <= std::min(e64, e32)) return kTile128;
   return e64 <= e32 ? kTile64 : kTile32;
