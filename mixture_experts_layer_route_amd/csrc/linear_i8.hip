@@ -334,14 +334,11 @@ template <int BK> __device__ __forceinline__ int i8_swz(int row) {
   return BK == 64 ? (row >> 2) & 3 : BK == 128 ? (row >> 1) & 7 : row & 15;
 }
 
-#ifndef MOE_I8_GM
-#define MOE_I8_GM 4
-#endif
-// Tile of a workgroup: workgroup b runs on XCD b % 8, every XCD takes one contiguous run of
-// the tiles in an order that walks GM token tiles per weight tile, so that the tiles in flight
+// Tile of a workgroup: workgroup b runs on XCD b % 8, every XCD takes one contiguous run
+// of the tiles in an order that walks GM token tiles per weight tile, so that the tiles in flight
 // on an XCD share rows and weights in its L2.
 __device__ __forceinline__ bool i8_tile_item(int mtiles, int ntiles, int& mt, int& nt) {
-  constexpr int GM = MOE_I8_GM;
+  constexpr int GM = 4;     // (2 and 8 measured alike)
   const int n = mtiles * ntiles, per = (n + 7) >> 3;
   const int j = int(blockIdx.x & 7) * per + int(blockIdx.x >> 3);
   if (int(blockIdx.x >> 3) >= per || j >= n) return false;
@@ -352,88 +349,132 @@ __device__ __forceinline__ bool i8_tile_item(int mtiles, int ntiles, int& mt, in
   return true;
 }
 
-// A wave's accumulators -> outputs, through 32-row pieces in LDS that only this wave uses:
-// a lane holds 4 consecutive columns of one token per block, and leaves with 8
-// consecutive columns of a token, so that stores are 16 bytes and contiguous over the lanes.
-template <typename TO, bool GLU, class C>
+// A wave's accumulators -> outputs.  A lane holds four consecutive columns of one token per
+// block (for a gated product the gate's and the up's), so the arithmetic is done there; the
+// results then pass through a 32-token piece of LDS that only this wave uses, to leave as 16
+// bytes per lane, contiguous over the lanes.  ST is the type they are staged in: the output's
+// own, or fp32 where a residual is still to be added before the rounding.
+// sx, sw: the scales of the wave's tokens and weight rows, in LDS.
+template <typename TO, typename ST, bool GLU, class C>
 __device__ __forceinline__ void i8_epilogue(unsigned char* stg, const i32x4 (&acc)[C::FN][C::FM],
                                             const I8Args& a, int64_t tw, int nw, int lane,
                                             const float* sx, const float* sw) {
+  constexpr bool H16 = std::is_same<TO, h16_t>::value;
+  constexpr int FO = GLU ? C::FN / 2 : C::FN, OC = FO * 16;   // output blocks and columns
+  constexpr int EPL = sizeof(ST) == 4 && sizeof(TO) == 4 ? 4 : 8;   // elements a lane leaves with
+  constexpr int LPR = OC / EPL, RPP = 64 / LPR;               // lanes per row, rows per pass
+  constexpr int RS = OC * sizeof(ST) + 16;                    // bytes per staged row
   const int64_t T = a.T;
   const int N = a.N;
-  constexpr int RS = C::TN + 4;                       // ints per staged row
-  constexpr int OC = GLU ? C::TN / 2 : C::TN;
-  constexpr int LPR = OC / 8, RPP = 64 / LPR;         // lanes per row, rows per pass
-  int* const st = reinterpret_cast<int*>(stg);
-  const int c8 = (lane % LPR) * 8, n = nw + c8;
-  float s0[8], s1[8];
+  const int l16 = lane & 15, q = lane >> 4;
+  float s0[FO][4], s1[FO][4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    s0[i] = sw[c8 + i];
-    s1[i] = GLU ? sw[OC + c8 + i] : 0.f;
-  }
+  for (int f = 0; f < FO; ++f)
 #pragma unroll
-  for (int m = 0; m < C::FM / 2; ++m) {
+    for (int r = 0; r < 4; ++r) {
+      s0[f][r] = sw[f * 16 + 4 * q + r];
+      s1[f][r] = GLU ? sw[OC + f * 16 + 4 * q + r] : 0.f;
+    }
+  const int ce = (lane % LPR) * EPL, n = nw + ce;
 #pragma unroll
-    for (int f = 0; f < C::FN; ++f)
+  for (int mp = 0; mp < C::FM / 2; ++mp) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
-        *reinterpret_cast<i32x4*>(st + (16 * e + (lane & 15)) * RS + f * 16 + 4 * (lane >> 4)) =
-            acc[f][2 * m + e];
+    for (int e = 0; e < 2; ++e) {
+      const int m = 2 * mp + e;
+      const float ts = sx[m * 16 + l16];
+      float v[FO][4];
+#pragma unroll
+      for (int f = 0; f < FO; ++f)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          v[f][r] = i8_scaled(acc[f][m][r], ts, s0[f][r]);
+          if (GLU) {
+            const float u = i8_scaled(acc[FO + f][m][r], ts, s1[f][r]);
+            v[f][r] = (sizeof(TO) == 4 ? silu(v[f][r]) : silu16(v[f][r])) * u;
+          }
+        }
+      unsigned char* const row = stg + (16 * e + l16) * RS + 4 * q * sizeof(ST);
+      if constexpr (H16) {
+        // the wave's 32 columns are one group; four lanes hold a token's part of it
+        static_assert(GLU && OC == 32, "groups of 32 columns");
+        float mx = 0.f;
+#pragma unroll
+        for (int f = 0; f < FO; ++f)
+          if (nw + f * 16 < N) {                         // (N is a multiple of 16 here)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) mx = fmaxf(mx, fabsf(v[f][r]));
+          }
+        mx = fmaxf(mx, __shfl_xor(mx, 16));
+        mx = fmaxf(mx, __shfl_xor(mx, 32));
+        const int64_t t = tw + m * 16 + l16;
+        if (q == 0 && t < T && nw < N) a.hmax[t * ((N + 31) / 32) + nw / 32] = mx;
+        const float up = mx >= 1.17549435e-38f ? 32767.0f / mx : 0.0f;
+#pragma unroll
+        for (int f = 0; f < FO; ++f) {
+          uint32_t w[2];
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+            w[r] = (uint32_t(int(rintf(v[f][2 * r] * up))) & 0xFFFFu) |
+                   (uint32_t(int(rintf(v[f][2 * r + 1] * up))) << 16);
+          *reinterpret_cast<uint2*>(row + f * 32) = make_uint2(w[0], w[1]);
+        }
+      } else if constexpr (sizeof(ST) == 4) {
+#pragma unroll
+        for (int f = 0; f < FO; ++f)
+          *reinterpret_cast<float4*>(row + f * 64) = make_float4(v[f][0], v[f][1], v[f][2], v[f][3]);
+      } else {
+#pragma unroll
+        for (int f = 0; f < FO; ++f)
+          *reinterpret_cast<uint2*>(row + f * 32) =
+              make_uint2(uint32_t(f32_to_bf16(v[f][0])) | (uint32_t(f32_to_bf16(v[f][1])) << 16),
+                         uint32_t(f32_to_bf16(v[f][2])) | (uint32_t(f32_to_bf16(v[f][3])) << 16));
+      }
+    }
 #pragma unroll
     for (int p = 0; p < 32 / RPP; ++p) {
       const int row = p * RPP + lane / LPR;
-      const int64_t t = tw + m * 32 + row;
-      const i32x4 a0 = *reinterpret_cast<const i32x4*>(st + row * RS + c8);
-      const i32x4 a1 = *reinterpret_cast<const i32x4*>(st + row * RS + c8 + 4);
-      const float ts = sx[m * 32 + row];
-      float v[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = i8_scaled(i < 4 ? a0[i & 3] : a1[i & 3], ts, s0[i]);
-      if (GLU) {
-        const i32x4 b0 = *reinterpret_cast<const i32x4*>(st + row * RS + OC + c8);
-        const i32x4 b1 = *reinterpret_cast<const i32x4*>(st + row * RS + OC + c8 + 4);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float u = i8_scaled(i < 4 ? b0[i & 3] : b1[i & 3], ts, s1[i]);
-          v[i] = (sizeof(TO) == 4 ? silu(v[i]) : silu16(v[i])) * u;
-        }
-      }
-      if constexpr (std::is_same<TO, h16_t>::value) {
-        // a wave's 32 columns are one group, four lanes of a quad hold a row of it
-        static_assert(GLU && OC == 32, "groups of 32 columns");
-        float m = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) m = fmaxf(m, n < N ? fabsf(v[i]) : 0.f);
-        m = fmaxf(m, dppf<0xB1>(m));    // quad_perm [1,0,3,2]
-        m = fmaxf(m, dppf<0x4E>(m));    // quad_perm [2,3,0,1]
-        if (t >= T || n >= N) continue;
-        const float up = m >= 1.17549435e-38f ? 32767.0f / m : 0.0f;
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          w[i] = (uint32_t(int(rintf(v[2 * i] * up))) & 0xFFFFu) | (uint32_t(int(rintf(v[2 * i + 1] * up))) << 16);
-        *reinterpret_cast<uint4*>(static_cast<int16_t*>(a.y) + t * N + n) = make_uint4(w[0], w[1], w[2], w[3]);
-        if (lane % LPR == 0) a.hmax[t * ((N + 31) / 32) + n / 32] = m;
-        continue;
-      } else {
-      const TO* const res = static_cast<const TO*>(a.res);
-      TO* const y = static_cast<TO*>(a.y);
+      const int64_t t = tw + mp * 32 + row;
+      const unsigned char* const from = stg + row * RS + ce * sizeof(ST);
       if (t >= T || n >= N) continue;
       const int64_t at = t * N + n;
-      if (a.vec) {
-        if (res) {
-          float r[8];
-          load8(res + at, r);
+      if constexpr (sizeof(ST) == 2) {
+        const uint4 o = *reinterpret_cast<const uint4*>(from);
+        if (a.vec) {
+          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.y) + at) = o;
+        } else {
+          const uint32_t w[4] = {o.x, o.y, o.z, o.w};
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] += r[i];
+          for (int i = 0; i < 8; ++i)
+            if (n + i < N) static_cast<uint16_t*>(a.y)[at + i] = uint16_t(w[i / 2] >> (16 * (i % 2)));
         }
-        store8(y + at, v);
       } else {
+        const TO* const res = static_cast<const TO*>(a.res);
+        TO* const y = static_cast<TO*>(a.y);
+        float v[EPL];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (n + i < N) y[at + i] = from_f32<TO>(res ? v[i] + to_f32<TO>(res[at + i]) : v[i]);
-      }
+        for (int i = 0; i < EPL / 4; ++i) {
+          const float4 o = *reinterpret_cast<const float4*>(from + 16 * i);
+          v[4 * i] = o.x; v[4 * i + 1] = o.y; v[4 * i + 2] = o.z; v[4 * i + 3] = o.w;
+        }
+        if (a.vec) {
+          if constexpr (EPL == 4) {
+            if (res) {
+              const float4 r = *reinterpret_cast<const float4*>(res + at);
+              v[0] += r.x; v[1] += r.y; v[2] += r.z; v[3] += r.w;
+            }
+            *reinterpret_cast<float4*>(y + at) = make_float4(v[0], v[1], v[2], v[3]);
+          } else {
+            float r[8];
+            load8(res + at, r);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] += r[i];
+            store8(y + at, v);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < EPL; ++i)
+            if (n + i < N) y[at + i] = from_f32<TO>(res ? v[i] + to_f32<TO>(res[at + i]) : v[i]);
+        }
       }
     }
   }
@@ -454,7 +495,7 @@ struct I8Tile {
   static constexpr bool WHOLE = 4 * (FM * FN + 2 * KS * (FM + FN)) <= 144;
   static constexpr int SLAB = (BM + BN) * BK;                          // bytes
   static constexpr int L = SLAB / 1024 / NW;                           // loads per lane and slab
-  static constexpr int STG = 32 * (TN + 4) * 4;                        // epilogue bytes per wave
+  static constexpr int STG = 32 * (TN * 4 + 16);                       // epilogue bytes per wave
   static constexpr int RED = FM * FN * 1024;                           // a wave's sums
   static constexpr int END = NP * (STG > (KW - 1) * RED ? STG : (KW - 1) * RED);
   static constexpr int RING = S * SLAB > END ? S * SLAB : END;
@@ -491,8 +532,9 @@ __device__ __forceinline__ void i8_slab_sync() {
 // slot is refilled as soon as the last fragments of it are in registers, half a phase before
 // the slab's end, which is also where the one barrier per slab is; each phase's fragments are
 // read during the phase before.
-// 8192 x 4096 x 8192: 226 us, 2.43e15 op/s; 8192 x 8192 x 2048: 111 us, 2.47e15; gated 4096 x
-// 2048 x 8192: 132 us, 2.09e15.
+// 8192 x 4096 x 8192: 221 us, 2.49e15 op/s; 8192 x 8192 x 2048: 109 us, 2.52e15; gated 4096 x
+// 2048 x 8192: 129 us, 2.13e15.  A persistent form that loads the next tile's first slab while the
+// results leave was slower (238 us for the first: it spills 30 registers).
 template <typename TO, bool GLU, class C>
 __global__ __launch_bounds__(C::NW * 64) void k_i8_tile(I8Args a) {
   constexpr int OC = GLU ? C::TN / 2 : C::TN;              // output columns per wave
@@ -500,20 +542,23 @@ __global__ __launch_bounds__(C::NW * 64) void k_i8_tile(I8Args a) {
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
   const int pos = wv % C::NP, kw = wv / C::NP;
   const int wm = pos / C::NWN, wn = pos % C::NWN;
-  int mt, nt;
-  if (!i8_tile_item(a.mtiles, a.ntiles, mt, nt)) return;
   const int64_t T = a.T;
   const int K = a.K, N = a.N;
+
+  int mt, nt;
+  if (!i8_tile_item(a.mtiles, a.ntiles, mt, nt)) return;
   const int64_t t0 = int64_t(mt) * C::BM;
   const int n0 = nt * (GLU ? C::BN / 2 : C::BN);
 
-  // one load instruction of a wave fills 64 / CPR rows; lane L writes chunk position L % CPR
+  // one load instruction of a wave fills 64 / CPR rows; lane L writes chunk position L % CPR, of
+  // rows that are equal modulo the swizzle's period in all of its loads
+  constexpr int RPL = 64 / C::CPR;
+  static_assert(C::NW * RPL % 16 == 0, "one chunk for all loads of a lane");
+  const int kc = ((lane % C::CPR) ^ i8_swz<C::BK>(wv * RPL + lane / C::CPR)) * 16;
   const int8_t* src[C::L];
-  int kc[C::L];
 #pragma unroll
   for (int i = 0; i < C::L; ++i) {
-    const int r = (wv + C::NW * i) * (64 / C::CPR) + lane / C::CPR;
-    kc[i] = ((lane % C::CPR) ^ i8_swz<C::BK>(r)) * 16;
+    const int r = (wv + C::NW * i) * RPL + lane / C::CPR;
     if (r < C::BM) {
       src[i] = a.x + min<int64_t>(t0 + r, T - 1) * K;
     } else {
@@ -536,14 +581,8 @@ __global__ __launch_bounds__(C::NW * 64) void k_i8_tile(I8Args a) {
   }
   const int nk = (K + C::BK - 1) / C::BK;
   auto load = [&](int i, int kt, int slot) {
-    dma16(src[i] + min(kt * C::BK + kc[i], K - 16), lds + slot * C::SLAB + (wv + C::NW * i) * 1024);
+    dma16(src[i] + min(kt * C::BK + kc, K - 16), lds + slot * C::SLAB + (wv + C::NW * i) * 1024);
   };
-
-  i32x4 acc[C::FN][C::FM];
-#pragma unroll
-  for (int n = 0; n < C::FN; ++n)
-#pragma unroll
-    for (int m = 0; m < C::FM; ++m) acc[n][m] = i32x4{0, 0, 0, 0};
 
   const int l16 = lane & 15, q = lane >> 4;
   int foff[C::KS];                                       // this lane's chunk of each MFMA step
@@ -561,6 +600,11 @@ __global__ __launch_bounds__(C::NW * 64) void k_i8_tile(I8Args a) {
 #pragma unroll
       for (int i = 0; i < C::L; ++i) load(i, k, k);
     }
+  i32x4 acc[C::FN][C::FM];
+#pragma unroll
+  for (int n = 0; n < C::FN; ++n)
+#pragma unroll
+    for (int m = 0; m < C::FM; ++m) acc[n][m] = i32x4{0, 0, 0, 0};
   if (nk >= C::S) i8_slab_sync<(C::S - 1) * C::L>(); else i8_slab_sync<0>();
   int slot = 0;
   using Buf0 = std::integral_constant<int, 0>;
@@ -687,8 +731,16 @@ __global__ __launch_bounds__(C::NW * 64) void k_i8_tile(I8Args a) {
     __syncthreads();
     if (kw > 0) return;
   }
-  i8_epilogue<TO, GLU, C>(lds + pos * C::STG, acc, a, t0 + wm * C::TM, n0 + wn * OC, lane,
-                          scales + wm * C::TM, scales + C::BM + wn * C::TN);
+  auto leave = [&](auto staged) {
+    i8_epilogue<TO, decltype(staged), GLU, C>(lds + pos * C::STG, acc, a, t0 + wm * C::TM,
+                                              n0 + wn * OC, lane, scales + wm * C::TM,
+                                              scales + C::BM + wn * C::TN);
+  };
+  if constexpr (sizeof(TO) == 2 && !GLU) {
+    if (a.res) leave(0.f); else leave(TO());
+  } else {
+    leave(TO());
+  }
 }
 
 static I8Args i8_args(const I8Product& p) {
