@@ -769,39 +769,48 @@ static void launch_tile(const I8Product& p, hipStream_t st, float* hmax = nullpt
   hipLaunchKernelGGL((k_i8_tile<TO, GLU, C>), dim3(xcd_grid(mt * nt)), dim3(C::NW * 64), 0, st, a);
 }
 
-// The tiles: one workgroup of the largest per CU, two or three of the smaller ones.
+// The tiles: one workgroup per CU of 256, 128 and 64 deep (96 to 130 KB of LDS), two or three of
+// the others.
 using Tile256 = I8Tile<256, 256, 2, 4, 128, 2>;
-using Tile128 = I8Tile<128, 128, 2, 4, 128, 3>;
+using Tile128 = I8Tile<128, 128, 4, 2, 128, 3>;
+using Tile64Deep = I8Tile<64, 64, 1, 2, 256, 3, 4>;
 using Tile64 = I8Tile<64, 64, 2, 2, 128, 3, 2>;
 using Tile32 = I8Tile<32, 64, 1, 2, 256, 3, 4>;
 
 // Which kernel: up to 16 tokens (32 without the gate) the weights are streamed past every
 // token at once; beyond, the tile whose estimated time is least.  The estimate is
-//   (128-wide K slabs) * max(one slab alone, tiles per CU * a slab among others) + start and end
-// fitted to measurements from 64 to 8192 tokens (us: alone 0.30 / 0.26 / 0.56, among others
-// 0.20 / 0.25 / 0.65, start and end 2.2 / 3.3 / 4 for 32x64, 64x64, 128x128; a round of
-// 256x256 tiles, one per CU, takes 1.65 a slab and 4).  The smaller tiles share a CU, so a part
-// of a round costs a part of it; the largest pays whole rounds.
+//   (128-wide K slabs) * (tiles on the fullest CU) * (time of a slab) + (start and end),
+// fitted to measurements from 64 to 8192 tokens and widths from 1040 to 8192 (us a slab: 0.19,
+// 0.26, 0.56 alone and 0.65 among others for 32x64, 64x64, 128x128; start and end 2.8, 3.3, 3.7;
+// the deep 64x64 tile 0.20 and 3.9, where every tile has a CU of its own; a round of 256x256
+// tiles 1.6 and 4).
 // Measured on either side of a switch (us): 64 x 1536 x 4096 few 5.9, 32x64 5.1, 64x64 6.4;
-// 512 x 2048 x 2048 32x64 8.7, 64x64 8.4, 128x128 12.9; 2048 x 2048 x 2048 64x64 19.6, 128x128
-// 15.0; 8192 x 8192 x 2048 128x128 164, 256x256 111; gated 333 x 1536 x 4112 64x64 14.8,
-// 128x128 11.8.
-enum I8Kernel { kFew16, kFew32, kTile32, kTile64, kTile128, kTile256 };
+// 200 x 1536 x 1536 32x64 5.1, deep 6.1; 512 x 2048 x 2048 32x64 8.8, 64x64 8.4, deep 7.7, 128x128
+// 12.3; 2048 x 2048 x 2048 64x64 18.3, deep 25.5, 128x128 14.1; 8192 x 8192 x 2048 128x128 148,
+// 256x256 109; gated 333 x 1536 x 4112 64x64 14.1, 128x128 11.1.
+enum I8Kernel { kFew16, kFew32, kTile32, kTile64, kTile64Deep, kTile128, kTile256 };
 static I8Kernel pick_kernel(int64_t T, int K, int N, bool glu) {
   if (T <= 16) return kFew16;
   if (T <= 32 && !glu) return kFew32;
   const double slabs = double((K + 127) / 128);
-  auto tiles = [&](int bm, int bn) {
+  auto per_cu = [&](int bm, int bn) {
     const int oc = glu ? bn / 2 : bn;
-    return double((T + bm - 1) / bm) * double((N + oc - 1) / oc) / 256.0;
+    return std::ceil(double((T + bm - 1) / bm) * double((N + oc - 1) / oc) / 256.0);
   };
-  const double e256 = std::ceil(tiles(256, 256)) * (slabs * 1.65 + 4.0);
-  const double e128 = slabs * std::max(0.56, tiles(128, 128) * 0.65) + 4.0;
-  const double e64 = slabs * std::max(0.26, tiles(64, 64) * 0.25) + 3.3;
-  const double e32 = slabs * std::max(0.30, tiles(32, 64) * 0.20) + 2.2;
-  if (e256 <= std::min(e128, std::min(e64, e32))) return kTile256;
-  if (e128 <= std::min(e64, e32)) return kTile128;
-  return e64 <= e32 ? kTile64 : kTile32;
+  const double c64 = per_cu(64, 64), c128 = per_cu(128, 128);
+  double least = slabs * per_cu(32, 64) * 0.19 + 2.8;
+  I8Kernel pick = kTile32;
+  auto offer = [&](I8Kernel k, double us) {
+    if (us < least) {
+      least = us;
+      pick = k;
+    }
+  };
+  offer(kTile64, slabs * c64 * 0.26 + 3.3);
+  if (c64 == 1.0) offer(kTile64Deep, slabs * 0.20 + 3.9);
+  offer(kTile128, slabs * (c128 == 1.0 ? 0.56 : c128 * 0.65) + 3.7);
+  offer(kTile256, per_cu(256, 256) * (slabs * 1.6 + 4.0));
+  return pick;
 }
 bool glu_h16_ok(int64_t T, int K, int N) { return pick_kernel(T, K, N, true) == kTile256; }
 
@@ -814,6 +823,7 @@ static int launch_product(const I8Product& p, hipStream_t st) {
       break;
     case kTile32: launch_tile<TO, GLU, Tile32>(p, st); break;
     case kTile64: launch_tile<TO, GLU, Tile64>(p, st); break;
+    case kTile64Deep: launch_tile<TO, GLU, Tile64Deep>(p, st); break;
     case kTile128: launch_tile<TO, GLU, Tile128>(p, st); break;
     case kTile256: launch_tile<TO, GLU, Tile256>(p, st); break;
   }

@@ -188,7 +188,8 @@ def check_product(y, p, res, dt):
 SHAPES = [(1, 16, 1), (1, 1536, 4096), (2, 48, 17), (4, 128, 33), (15, 144, 100), (16, 2048, 64),
           (17, 272, 15), (31, 1040, 130), (33, 400, 24), (64, 1536, 48), (65, 1536, 72), (77, 1040, 1001),
           (100, 16, 256), (128, 128, 128), (129, 64, 129), (200, 2064, 384), (255, 80, 257),
-          (300, 96, 1000), (513, 1536, 520), (1000, 208, 2000), (1025, 512, 2049), (2500, 4096, 1000),
+          (300, 96, 1000), (513, 1536, 520), (513, 2064, 2041),
+          (505, 2064, 1999), (1000, 208, 2000), (1025, 512, 2049), (2500, 4096, 1000),
           (8100, 4112, 2041), (7937, 8192, 2048)]
 
 
@@ -210,7 +211,7 @@ def test_linear_i8(moe, T, K, N):
 
 
 @pytest.mark.parametrize("T,K,N", [(1, 1536, 5120), (4, 48, 33), (16, 2048, 64), (31, 1040, 130),
-                                   (64, 272, 48), (100, 1536, 200), (130, 64, 129), (333, 1536, 1040),
+                                   (64, 272, 48), (100, 1536, 200), (130, 64, 129), (333, 1536, 1040), (333, 1552, 4107),
                                    (1025, 400, 2056), (2500, 2048, 1000),
                                    (8100, 2064, 1021), (7937, 4096, 1024)])
 def test_glu_i8(moe, T, K, N):
