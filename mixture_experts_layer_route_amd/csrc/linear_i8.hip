@@ -14,11 +14,8 @@ __device__ __forceinline__ float i8_scaled(int acc, float sx, float sw) { return
 
 // Four consecutive outputs of one row (n .. n+3; `vec`: rows are 16-byte aligned, N % 8 == 0).
 template <typename TO>
-__device__ __forceinline__ void store_out4(TO* y, const TO* res, int64_t row_off, int n, int N,
-                                           bool vec, float (&v)[4]) {
-#pragma unroll
-  for (int r = 0; r < 4; ++r)
-    if (res && n + r < N) v[r] += to_f32<TO>(res[row_off + n + r]);
+__device__ __forceinline__ void store_out4(TO* y, int64_t row_off, int n, int N, bool vec,
+                                           const float (&v)[4]) {
   if (vec) {
     if (n >= N) return;
     if constexpr (sizeof(TO) == 4) {
@@ -80,6 +77,9 @@ __host__ __device__ inline int few_stride(int K) { return (K + 255) / 256 * 256 
 // loads, so that the weights' can follow before the first value is waited for.
 template <typename TA, int NCH>
 struct FewNorm {
+  // two workgroups per CU where the rows' registers allow it (a grid is often a little over one
+  // workgroup per CU: 5120 columns at 130 registers ran as two rounds, 10.3 us against 7.6)
+  static constexpr int WAVES = sizeof(TA) * NCH <= 8 ? 4 : 2;
   Chunk8<TA> x[2][NCH], g[NCH];
   __device__ __forceinline__ void load(const I8Args& a, int lane, int wv) {
 #pragma unroll
@@ -140,6 +140,7 @@ struct FewNorm {
 // comes from its tiles' maxima, so h is read once; a lane's first chunks and maxima are on
 // their way before the weights.
 struct FewQuant {
+  static constexpr int WAVES = 4;
   static constexpr int PRE = 2, HM = 6;
   Chunk8<float> h[2][PRE];
   float hm[2][HM];
@@ -191,6 +192,7 @@ struct FewQuant {
   }
 };
 struct FewNone {
+  static constexpr int WAVES = 4;
   __device__ __forceinline__ void load(const I8Args&, int, int) {}
   __device__ __forceinline__ void store(const I8Args&, int, int, int8_t*, float*) {}
 };
@@ -205,7 +207,7 @@ struct FewNone {
 // beside the two in use.
 // T <= 16 TB; grid = ceil(N / 16), block = 512, dynamic LDS = T * few_stride(K) unless kCodes.
 template <typename TO, int TB, bool GLU, FewSrc SRC, class Make>
-__global__ __launch_bounds__(512) void k_i8_few(I8Args a) {
+__global__ __launch_bounds__(512, Make::WAVES) void k_i8_few(I8Args a) {
   constexpr int NW = 8, NA = GLU ? 2 : 1;
   __shared__ i32x4 part[NW][NA * TB][64];
   __shared__ float own_sx[16];
@@ -262,6 +264,23 @@ __global__ __launch_bounds__(512) void k_i8_few(I8Args a) {
         for (int b = 0; b < TB; ++b)
           acc[i][b] = __builtin_amdgcn_mfma_i32_16x16x64_i8(f.w[i][h], f.x[b][h], acc[i][b], 0, 0, 0);
   };
+  // What the end needs of scales and residual follows the first weights: after the sums it would
+  // be one more round trip to cold memory (layer of one token, down product 6.4 against 5.9 us),
+  // before the token rows it would delay their codes.  With the norm in front there are no
+  // registers for it (9.3 us with, 7.6 without).
+  const int ob = min(wv, TB - 1), on = n0 + 4 * q, ot = 16 * ob + r16;
+  float es0[4], es1[4] = {0.f, 0.f, 0.f, 0.f}, er[4] = {0.f, 0.f, 0.f, 0.f}, est = 0.f;
+  auto load_end = [&] {
+    if (wv >= TB) return;
+    if (SRC == kCodes) est = a.sx[min(ot, T - 1)];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int nr = min(on + r, N - 1);
+      es0[r] = a.sw[nr];
+      if (GLU) es1[r] = a.su[nr];
+      if (a.res) er[r] = to_f32<TO>(static_cast<const TO*>(a.res)[int64_t(min(ot, T - 1)) * N + nr]);
+    }
+  };
   Unit f0, f1;
   int u = wv;
   Make make;
@@ -269,8 +288,10 @@ __global__ __launch_bounds__(512) void k_i8_few(I8Args a) {
   if (u < nu) load_w(u, f0);
   if (SRC == kCodes) {
     if (u < nu) load_x(u, f0);
+    load_end();
   } else {
     if (u + NW < nu) load_w(u + NW, f1);
+    if (SRC != kNorm) load_end();
     make.store(a, lane, wv, own_codes, own_sx);
     __syncthreads();
   }
@@ -298,8 +319,8 @@ __global__ __launch_bounds__(512) void k_i8_few(I8Args a) {
   __syncthreads();
   // a wave per 16 tokens, a thread per four outputs: columns n .. n + 3 of token t
   if (wv >= TB) return;
-  const int b = wv, n = n0 + 4 * q;
-  const int t = 16 * b + r16;
+  if (SRC == kNorm) load_end();
+  const int b = wv, n = on, t = ot;
   i32x4 s[NA];
 #pragma unroll
   for (int i = 0; i < NA; ++i) {
@@ -307,13 +328,13 @@ __global__ __launch_bounds__(512) void k_i8_few(I8Args a) {
 #pragma unroll
     for (int k = 1; k < NW; ++k) s[i] += part[k][i * TB + b][lane];
   }
-  const float st = SRC == kCodes ? a.sx[min(t, T - 1)] : own_sx[min(t, T - 1)];
+  const float st = SRC == kCodes ? est : own_sx[min(t, T - 1)];
   float v[4];
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
-    const int nr = min(n + r, N - 1);
-    v[r] = i8_scaled(s[0][r], st, a.sw[nr]);
-    if (GLU) v[r] = silu(v[r]) * i8_scaled(s[NA - 1][r], st, a.su[nr]);
+    v[r] = i8_scaled(s[0][r], st, es0[r]);
+    if (GLU) v[r] = silu(v[r]) * i8_scaled(s[NA - 1][r], st, es1[r]);
+    if (!GLU) v[r] += er[r];                 // (zeros without a residual)
   }
   if (SRC == kNorm) {
     float m = 0.f;
@@ -325,7 +346,7 @@ __global__ __launch_bounds__(512) void k_i8_few(I8Args a) {
     if (q == 0 && t < T) a.hmax[int64_t(t) * gridDim.x + blockIdx.x] = m;
   }
   if (t < T)
-    store_out4<TO>(static_cast<TO*>(a.y), static_cast<const TO*>(a.res), int64_t(t) * N, n, N, a.vec, v);
+    store_out4<TO>(static_cast<TO*>(a.y), int64_t(t) * N, n, N, a.vec, v);
 }
 
 // 16-byte chunks of the tile's LDS rows are XOR-swizzled so that the 16 consecutive rows one
@@ -376,8 +397,27 @@ __device__ __forceinline__ void i8_epilogue(unsigned char* stg, const i32x4 (&ac
       s1[f][r] = GLU ? sw[OC + f * 16 + 4 * q + r] : 0.f;
     }
   const int ce = (lane % LPR) * EPL, n = nw + ce;
+  // the residual of a piece is loaded a piece ahead (y may be the residual itself, so the
+  // compiler could not move a load over the stores before it)
+  constexpr int PP = 32 / RPP;                                // passes per piece
+  constexpr bool RES = sizeof(ST) == 4 && !GLU;
+  uint4 rb[2][RES ? PP : 1];
+  auto load_res = [&](int mp, uint4 (&r)[RES ? PP : 1]) {
+#pragma unroll
+    for (int p = 0; p < PP; ++p) {
+      const int64_t t = min<int64_t>(tw + mp * 32 + p * RPP + lane / LPR, T - 1);
+      r[p] = *reinterpret_cast<const uint4*>(static_cast<const TO*>(a.res) + t * N + min(n, N - EPL));
+    }
+  };
+  const bool fast_res = RES && a.res && a.vec;
+  if constexpr (RES) {
+    if (fast_res) load_res(0, rb[0]);
+  }
 #pragma unroll
   for (int mp = 0; mp < C::FM / 2; ++mp) {
+    if constexpr (RES) {
+      if (fast_res && mp + 1 < C::FM / 2) load_res(mp + 1, rb[(mp + 1) & 1]);
+    }
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int m = 2 * mp + e;
@@ -458,14 +498,18 @@ __device__ __forceinline__ void i8_epilogue(unsigned char* stg, const i32x4 (&ac
         }
         if (a.vec) {
           if constexpr (EPL == 4) {
-            if (res) {
-              const float4 r = *reinterpret_cast<const float4*>(res + at);
-              v[0] += r.x; v[1] += r.y; v[2] += r.z; v[3] += r.w;
+            if constexpr (RES) {
+              if (fast_res) {
+                const float4 r = __builtin_bit_cast(float4, rb[mp & 1][p]);
+                v[0] += r.x; v[1] += r.y; v[2] += r.z; v[3] += r.w;
+              }
             }
             *reinterpret_cast<float4*>(y + at) = make_float4(v[0], v[1], v[2], v[3]);
           } else {
+            Chunk8<TO> c;
+            c.v = rb[mp & 1][p];
             float r[8];
-            load8(res + at, r);
+            c.get(r);
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] += r[i];
             store8(y + at, v);
