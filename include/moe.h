@@ -332,8 +332,10 @@ int moe_forward_paged(const moe_config* cfg, const void* x, const moe_weights* h
  * normal fp32 has scale 1 (code 0 of E8M0 for a zero MXFP8 block).  With norm_weight and
  * residual NULL the call quantises (MOE_ROWS_I8 over [out, in] weights gives the codes and
  * channel scales the products below take).
+ * The sum of squares is fp32: it has to stay finite, and squares below its range count as zero; a
+ * row of which nothing is left (with norm_eps 0 too) gives zeros.
  * act_dtype MOE_F32 or MOE_BF16; width a multiple of 8 (128 for E4M3_B128, 32 for MXFP8), at
- * most 32768; rows < 2^31.  x_sum (required with a residual, else ignored) may be x or
+ * most 32768; rows <= 2^21.  x_sum (required with a residual, else ignored) may be x or
  * residual, and a MOE_ROWS_ACT out may be x or residual; other overlaps are not allowed.
  * Scales need their own type's alignment only.
  */
@@ -351,8 +353,8 @@ int moe_norm_quant_rows(int64_t rows, int32_t width, int32_t act_dtype, int32_t 
  * x [rows, in_width], w [out_width, in_width] int8 (any codes, -128 included); scales fp32,
  * y and residual [rows, out_width] out_dtype (MOE_F32 or MOE_BF16), aligned to their type;
  * residual may be NULL or y itself.  The sum is exact (int32), so results do not depend on
- * the batch a row comes in.  in_width a multiple of 16, at most 65536; rows < 2^31,
- * out_width <= 2^30, rows * out_width <= 2^40.
+ * the batch a row comes in.  in_width a multiple of 16, at most 65536;
+ * rows <= 2^21, out_width <= 2^24, rows * out_width <= 2^35.
  */
 int moe_linear_i8(int64_t rows, int32_t in_width, int32_t out_width, int32_t out_dtype,
                   const int8_t* x, const float* x_scales, const int8_t* w, const float* w_scales,
@@ -371,8 +373,10 @@ int moe_glu_i8(int64_t rows, int32_t in_width, int32_t out_width, int32_t out_dt
  * A dense decoder layer's feed-forward block in 8 bits, the sibling of moe_forward_residual:
  *   x_out = round(x + down(i8(glu(i8(RMSNorm(x) * norm_weight)))))
  * with i8() the per-token quantisation of moe_norm_quant_rows; h is not rounded to act_dtype
- * between the products.  x, x_out [T, H] act_dtype; x_out may be x itself.  hidden and
- * intermediate are multiples of 16, at most 32768.  ws: moe_dense_workspace_size() bytes,
+ * between the products (it is held in fp32, or in 16 bits with a scale per row and 32 columns,
+ * 0.002 of a step of its codes apart from that).  x, x_out [T, H] act_dtype; x_out may be x
+ * itself.  hidden and intermediate are multiples of 16, at most 32768, T <= 2^21 and T times
+ * either at most 2^35.  ws: moe_dense_workspace_size() bytes,
  * 256-byte aligned.
  */
 typedef struct {

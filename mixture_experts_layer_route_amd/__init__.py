@@ -327,8 +327,8 @@ def _raw_stream(dev: int) -> int:
 
 
 def _device() -> int:
-    """The current device's index (-1 without one: every argument check then fails)."""
-    return torch._C._cuda_getDevice() if torch.cuda._initialized else -1
+    """The current device's index (-2, which no tensor has, before there is one)."""
+    return torch._C._cuda_getDevice() if torch.cuda._initialized else -2
 
 
 def _arg(name: str, t: torch.Tensor, shape: tuple, dtype: torch.dtype, dev: int) -> int:
@@ -336,13 +336,13 @@ def _arg(name: str, t: torch.Tensor, shape: tuple, dtype: torch.dtype, dev: int)
     device (the library launches on that device and checks nothing behind a pointer).  A call
     makes up to seven of these checks beside a launch of a few microseconds, so they use the
     cheapest accessors there are (get_device() of a host tensor is -1)."""
+    if (t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()):
+        return t.data_ptr()
     if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{name}: expected {dtype} {shape}, got {t.dtype} {tuple(t.shape)}")
-    if t.get_device() != dev or dev < 0:
+    if t.get_device() != dev:
         raise ValueError(f"{name}: expected a tensor on the current device, got {t.device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: contiguous tensors only")
-    return t.data_ptr()
+    raise ValueError(f"{name}: contiguous tensors only")
 
 
 def _act_dtype(name: str, dtype: torch.dtype) -> int:

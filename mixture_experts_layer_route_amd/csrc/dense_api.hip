@@ -25,7 +25,7 @@ static int check_norm_quant(const NormQuant& q) {
                    : q.format == MOE_ROWS_MXFP8                        ? 32
                                                                        : 0;
   if (!step || q.width % step || q.width > kNormMaxWidth) return MOE_ERR_UNSUPPORTED;
-  if (q.rows >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+  if (q.rows > kMaxRows) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
@@ -40,8 +40,7 @@ static int check_product(const I8Product& p, bool glu) {
   if ((reinterpret_cast<uintptr_t>(p.y) | reinterpret_cast<uintptr_t>(p.res)) & natural)
     return MOE_ERR_ARG;
   if (p.K % 16 || p.K > kI8MaxWidth) return MOE_ERR_UNSUPPORTED;
-  if (p.T >= (int64_t(1) << 31) || p.N > (1 << 30) || p.T > (int64_t(1) << 40) / p.N)
-    return MOE_ERR_UNSUPPORTED;   // (2^40 outputs: tile counts stay in 32 bits)
+  if (p.T > kMaxRows || p.N > kMaxColumns || p.T * p.N > kMaxOutputs) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
@@ -59,7 +58,8 @@ static int make_dense_plan(const moe_dense_config* c, DensePlan* out) {
   if (c->num_tokens < 1 || c->hidden < 1 || c->intermediate < 1) return MOE_ERR_ARG;
   if (c->act_dtype != MOE_F32 && c->act_dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
   if (c->hidden % 16 || c->intermediate % 16 || c->hidden > kNormMaxWidth ||
-      c->intermediate > kNormMaxWidth || c->num_tokens >= (int64_t(1) << 31))
+      c->intermediate > kNormMaxWidth || c->num_tokens > kMaxRows ||
+      c->num_tokens * std::max(c->hidden, c->intermediate) > kMaxOutputs)
     return MOE_ERR_UNSUPPORTED;
   DensePlan q{};
   q.T = c->num_tokens;

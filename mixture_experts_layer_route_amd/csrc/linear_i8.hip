@@ -110,7 +110,7 @@ struct FewNorm {
           ss += sj;
         }
       }
-      const float rinv = float(1.0 / sqrt(double(wave_sum(ss)) / a.K + double(a.eps)));
+      const float rinv = inv_rms(wave_sum(ss), a.K, a.eps);
       float m = 0.f;
 #pragma unroll
       for (int j = 0; j < NCH; ++j)

@@ -11,6 +11,10 @@ namespace moe {
 
 constexpr int kNormMaxWidth = 32768;    // widest row: 1024 threads x 4 chunks of 8
 constexpr int kI8MaxWidth = 65536;      // |sum| <= 65536 * 128 * 128 = 2^30: int32 sums are exact
+// A launch has fewer than 2^32 threads: rows (a workgroup of up to 1024 each in the norm), columns
+// (16 per workgroup of 512) and outputs (at least 8192 per workgroup of 512 where there are many)
+constexpr int64_t kMaxRows = int64_t(1) << 21, kMaxOutputs = int64_t(1) << 35;
+constexpr int kMaxColumns = 1 << 24;
 
 struct NormQuant {
   int64_t rows;
@@ -65,6 +69,12 @@ size_t dense_few_hmax_bytes(int64_t T, int I);
 int launch_dense_few(const DenseFew& d, hipStream_t st);
 
 #ifdef __HIPCC__
+// 1 / sqrt(mean square + eps) of a row: once per row, so in 64 bits (an error here would shift
+// every code of the row).  A row without squares and without eps is left as it is, at zero.
+__device__ __forceinline__ float inv_rms(float sum_sq, int width, float eps) {
+  const double ms = double(sum_sq) / width + double(eps);
+  return ms > 0.0 ? float(1.0 / sqrt(ms)) : 0.0f;
+}
 // Per-row int8: scale = amax / 127.  A row whose amax is so small that the scale would leave
 // the normal floats (or is zero) has scale 1 and codes 0, so no division overflows.
 __device__ __forceinline__ float i8_scale(float amax) {

@@ -81,8 +81,7 @@ __global__ __launch_bounds__(WPR == 16 ? 1024 : 256) void k_norm_quant(NormQuant
 #pragma unroll
       for (int i = 0; i < WPR; ++i) ss += part[wv / WPR * WPR + i];
     }
-    // once per row, in 64 bits: an error here would shift every code of the row
-    const float rinv = float(1.0 / sqrt(double(ss) / H + double(a.eps)));
+    const float rinv = inv_rms(ss, H, a.eps);
 #pragma unroll
     for (int j = 0; j < NCH; ++j) {
       const int c = j * 64 * WPR + pos;

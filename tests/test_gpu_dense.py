@@ -149,6 +149,9 @@ def test_norm_zero_tiny_and_huge_rows(moe, fmt):
     w = torch.ones(H, device="cuda")
     out, scales, _ = moe.norm_quant_rows(x[:2].contiguous(), fmt, w)
     check_rows(out, scales, fmt, mo.rms_norm(v[:2], np.ones(H), EPS), torch.float32)
+    # without eps a zero row stays zero, the others are normalised as ever
+    out, scales, _ = moe.norm_quant_rows(x[:2].contiguous(), fmt, w, eps=0.0)
+    check_rows(out, scales, fmt, np.stack([v[0], mo.rms_norm(v[1], np.ones(H), 0.0)]), torch.float32)
 
 
 def test_norm_in_place_and_neighbours(moe):
@@ -296,6 +299,7 @@ def layer(g, H, I, act):
                                        (4, 1536, 4112, "f32"), (9, 2048, 1040, "bf16"), (16, 4096, 8192, "bf16"),
                                        (17, 1536, 512, "bf16"), (16, 4112, 272, "bf16"), (64, 1536, 512, "f32"),
                                        (333, 1536, 4112, "bf16"), (2100, 512, 784, "bf16"), (16, 2048, 32768, "bf16"),
+                                       (16, 1536, 5120, "bf16"), (15, 1024, 8192, "f32"), (3, 4096, 32768, "bf16"),
                                        (4090, 2048, 8176, "bf16"), (7900, 2048, 4112, "f32")])
 def test_dense_layer(moe, T, H, I, act):
     """x_out against the oracle run through all four stages.

@@ -86,7 +86,7 @@ def _call(fn, base, **kw):
     (-1, dict(res=FAKE, x_sum=FAKE + 8)), (-1, dict(scales=FAKE + 2)),
     (-2, dict(act=2)), (-2, dict(act=-1)), (-2, dict(fmt=4)), (-2, dict(fmt=-1)),
     (-2, dict(width=1532)), (-2, dict(fmt=2, width=1600)), (-2, dict(fmt=3, width=1544)),
-    (-2, dict(width=32776)), (-2, dict(rows=1 << 31)),
+    (-2, dict(width=32776)), (-2, dict(rows=(1 << 21) + 1)), (-2, dict(rows=1 << 40)),
 ])
 def test_norm_quant_rows_refuses(lib, code, kw):
     assert _call(lib.moe_norm_quant_rows, ROWS, **kw) == code
@@ -97,7 +97,8 @@ BAD_PRODUCT = [
     (-1, dict(w=None)), (-1, dict(sw=None)), (-1, dict(y=None)), (-1, dict(x=FAKE + 8)),
     (-1, dict(w=FAKE + 1)), (-1, dict(sx=FAKE + 2)), (-1, dict(sw=FAKE + 1)), (-1, dict(y=FAKE + 1)),
     (-1, dict(out=0, y=FAKE + 2)), (-2, dict(out=2)), (-2, dict(K=1544)), (-2, dict(K=65552)),
-    (-2, dict(rows=1 << 31)), (-2, dict(N=(1 << 30) + 1)), (-2, dict(rows=1 << 25, N=(1 << 15) + 1)),
+    (-2, dict(rows=(1 << 21) + 1)), (-2, dict(rows=1 << 40)), (-2, dict(N=(1 << 24) + 1)),
+    (-2, dict(rows=1 << 21, N=(1 << 14) + 1)),
 ]
 
 
@@ -118,7 +119,7 @@ def test_dense_layer_refuses(lib):
     cfg = lambda *a: ctypes.byref(moe.make_dense_config(*a))
     for code, args in ((-1, (0, 1536, 512)), (-1, (4, 0, 512)), (-1, (4, 1536, 0)), (-2, (4, 1528, 512)),
                        (-2, (4, 1536, 520)), (-2, (4, 1536, 512, "e4m3")), (-2, (4, 32784, 512)),
-                       (-2, (4, 1536, 32784)), (-2, (1 << 31, 1536, 512))):
+                       (-2, (4, 1536, 32784)), (-2, ((1 << 21) + 1, 1536, 512)), (-2, (1 << 21, 512, 16400))):
         assert size(cfg(*args), ctypes.byref(n)) == code, args
     assert size(None, ctypes.byref(n)) == -1 and size(cfg(4, 1536, 512), None) == -1
     assert size(cfg(4, 1536, 512), ctypes.byref(n)) == 0 and n.value > 0
