@@ -856,7 +856,11 @@ static I8Kernel pick_kernel(int64_t T, int K, int N, bool glu) {
   offer(kTile256, per_cu(256, 256) * (slabs * 1.6 + 4.0));
   return pick;
 }
-bool glu_h16_ok(int64_t T, int K, int N) { return pick_kernel(T, K, N, true) == kTile256; }
+// (a wave of these two tiles has the 32 columns of a group)
+bool glu_h16_ok(int64_t T, int K, int N) {
+  const I8Kernel k = pick_kernel(T, K, N, true);
+  return k == kTile128 || k == kTile256;
+}
 
 template <typename TO, bool GLU>
 static int launch_product(const I8Product& p, hipStream_t st) {
@@ -875,7 +879,10 @@ static int launch_product(const I8Product& p, hipStream_t st) {
 }
 
 int launch_glu_h16(const I8Product& p, float* hmax, hipStream_t st) {
-  launch_tile<h16_t, true, Tile256>(p, st, hmax);
+  if (pick_kernel(p.T, p.K, p.N, true) == kTile128)
+    launch_tile<h16_t, true, Tile128>(p, st, hmax);
+  else
+    launch_tile<h16_t, true, Tile256>(p, st, hmax);
   return check_launch();
 }
 

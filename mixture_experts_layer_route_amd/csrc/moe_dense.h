@@ -46,7 +46,7 @@ struct I8Product {
 int launch_i8_product(const I8Product& p, hipStream_t st);
 
 // The gated product with h as int16 codes and group maxima ([T, N] and [T, ceil(N / 32)]; out is
-// ignored), where the widest tile is the one chosen; and the int8 codes of such rows.
+// ignored), where one of the two widest tiles is chosen; and the int8 codes of such rows.
 bool glu_h16_ok(int64_t T, int K, int N);
 int launch_glu_h16(const I8Product& p, float* hmax, hipStream_t st);
 int launch_h16_codes(const void* h, const float* hmax, int64_t T, int I, int8_t* codes, float* scales,
