@@ -402,3 +402,46 @@ def test_binding_refuses(moe):
         moe.glu_i8(x, sx, w, sw, w[:4], sw)
     with pytest.raises(ValueError):
         moe.norm_quant_rows(torch.zeros(4, 64, device="cuda"), "i8", torch.ones(60, device="cuda"))
+
+
+@pytest.mark.parametrize("T", [4, 300])
+def test_dense_layer_then_moe_block(moe, T):
+    """The start of a decoder stack: the dense layer 0, then an MoE block on the same residual
+    stream, eagerly and as one captured graph; the dense layer against the oracle, the block
+    bit for bit against the block run on the dense layer's output by itself."""
+    import synth
+    from tests.helpers import config_for, to_device
+    print("case: stack", T, flush=True)
+    shape = synth.WORKLOADS["decode"].with_tokens(T)
+    H, I = shape.H, 784
+    dev = to_device(synth.make_layer(shape))
+    mcfg, mwst = config_for(shape), moe.weights_struct(dev)
+    mws = moe.alloc_workspace(mcfg)
+    g = gen(T + 5)
+    w, gamma = layer(g, H, I, "bf16")
+    gamma2 = (1 + 0.1 * torch.randn(H, generator=g, device="cuda")).to(torch.bfloat16)
+    dcfg, dwst = moe.make_dense_config(T, H, I), moe.dense_weights_struct(w)
+    dws = moe.alloc_dense_workspace(dcfg)
+
+    def step(x):
+        x1 = moe.dense_residual_i8(dcfg, x, gamma, dwst, dws)
+        return x1, moe.forward_residual(mcfg, x1, gamma2, None, mws, wst=mwst)
+
+    x = dev["x"].clone()
+    x1, x2 = step(x)
+    ref = od.dense_layer(f64(x), f64(gamma), {k: f64(v) for k, v in w.items()})
+    err = np.maximum(np.abs(f64(x1) - ref) - store(torch.bfloat16) * np.abs(ref) * 1.0001, 0)
+    assert np.linalg.norm(err) <= 4e-3 * np.linalg.norm(ref - f64(x))
+    assert torch.equal(moe.forward_residual(mcfg, x1.clone(), gamma2, None, mws, wst=mwst), x2)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        g1, g2 = step(x)
+    for _ in range(3):
+        g1.zero_()
+        g2.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(g1, x1) and torch.equal(g2, x2)
+        step(torch.roll(x, 1, 0).contiguous())                # eager work on the same workspaces
+        torch.cuda.synchronize()
