@@ -577,8 +577,8 @@ __device__ __forceinline__ void i8_slab_sync() {
 // the slab's end, which is also where the one barrier per slab is; each phase's fragments are
 // read during the phase before.
 // 8192 x 4096 x 8192: 221 us, 2.49e15 op/s; 8192 x 8192 x 2048: 109 us, 2.52e15; gated 4096 x
-// 2048 x 8192: 129 us, 2.13e15.  A persistent form that loads the next tile's first slab while the
-// results leave was slower (238 us for the first: it spills 30 registers).
+// 2048 x 8192: 129 us, 2.13e15.  A persistent form that loads the next tile's first slabs while the
+// results leave was no faster (220 us for the first): on data the card's power bounds the rate.
 template <typename TO, bool GLU, class C>
 __global__ __launch_bounds__(C::NW * 64) void k_i8_tile(I8Args a) {
   constexpr int OC = GLU ? C::TN / 2 : C::TN;              // output columns per wave
