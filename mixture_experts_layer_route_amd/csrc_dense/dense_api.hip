@@ -48,7 +48,7 @@ static int check_product(const I8Product& p, bool glu) {
 struct DensePlan {
   int64_t T;
   int H, I, act;
-  bool few;                // up to 16 tokens: codes never leave the kernels
+  bool few;                // up to 8 tokens: codes never leave the kernels
   bool h16;                // wide batches: h as int16 codes with group maxima, else fp32
   size_t o_xq, o_sx, o_h, o_hq, o_sh, o_hmax, total;
 };

@@ -15,21 +15,22 @@ __device__ __forceinline__ float i8_scaled(int acc, float sx, float sw) { return
 // Four consecutive outputs of one row (n .. n+3; `vec`: rows are 16-byte aligned, N % 8 == 0).
 template <typename TO>
 __device__ __forceinline__ void store_out4(TO* y, int64_t row_off, int n, int N, bool vec,
-                                           const float (&v)[4]) {
+                                           float4 v) {
   if (vec) {
     if (n >= N) return;
     if constexpr (sizeof(TO) == 4) {
-      *reinterpret_cast<float4*>(y + row_off + n) = make_float4(v[0], v[1], v[2], v[3]);
+      *reinterpret_cast<float4*>(y + row_off + n) = v;
     } else {
       *reinterpret_cast<uint2*>(y + row_off + n) =
-          make_uint2(uint32_t(f32_to_bf16(v[0])) | (uint32_t(f32_to_bf16(v[1])) << 16),
-                     uint32_t(f32_to_bf16(v[2])) | (uint32_t(f32_to_bf16(v[3])) << 16));
+          make_uint2(uint32_t(f32_to_bf16(v.x)) | (uint32_t(f32_to_bf16(v.y)) << 16),
+                     uint32_t(f32_to_bf16(v.z)) | (uint32_t(f32_to_bf16(v.w)) << 16));
     }
     return;
   }
-#pragma unroll
-  for (int r = 0; r < 4; ++r)
-    if (n + r < N) y[row_off + n + r] = from_f32<TO>(v[r]);
+  if (n < N) y[row_off + n] = from_f32<TO>(v.x);
+  if (n + 1 < N) y[row_off + n + 1] = from_f32<TO>(v.y);
+  if (n + 2 < N) y[row_off + n + 2] = from_f32<TO>(v.z);
+  if (n + 3 < N) y[row_off + n + 3] = from_f32<TO>(v.w);
 }
 
 // What a kernel of this file reads and writes.  One argument by value: on the host a launch
@@ -72,127 +73,115 @@ constexpr int kFewCodes = 128 << 10;     // LDS bytes of codes a workgroup may m
 // (a row is a whole number of 256-byte bank lines for the usual widths).
 __host__ __device__ inline int few_stride(int K) { return (K + 255) / 256 * 256 + 16; }
 
-// RMSNorm and int8 codes of the rows wv, wv + 8 in LDS, by the definitions of k_norm_quant; a
-// wave per row with NCH chunks of 8 elements per lane (K <= 512 NCH).  load() only issues
-// loads, so that the weights' can follow before the first value is waited for.
-template <typename TA, int NCH>
+// RMSNorm and int8 codes of up to eight rows in LDS, by the definitions of k_norm_quant: wave wv
+// has row wv, four chunks of 8 elements per lane (K <= 2048).  load() only issues loads, so that
+// the weights' can follow before the first value is waited for.
+template <typename TA>
 struct FewNorm {
-  // two workgroups per CU where the rows' registers allow it (a grid is often a little over one
-  // workgroup per CU: 5120 columns at 130 registers ran as two rounds, 10.3 us against 7.6)
-  static constexpr int WAVES = sizeof(TA) * NCH <= 8 ? 4 : 2;
-  Chunk8<TA> x[2][NCH], g[NCH];
+  static constexpr int NCH = 4;
+  Chunk8<TA> x[NCH], g[NCH];
   __device__ __forceinline__ void load(const I8Args& a, int lane, int wv) {
+    if (wv >= a.T) return;                   // uniform over the wave
 #pragma unroll
     for (int j = 0; j < NCH; ++j) {
       const int c = j * 64 + lane;
       if (c < a.K / 8) {
-        if (wv < a.T) g[j].load(static_cast<const TA*>(a.gamma) + c * 8);
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          if (wv + 8 * i < a.T)
-            x[i][j].load(static_cast<const TA*>(a.rows) + int64_t(wv + 8 * i) * a.K + c * 8);
+        x[j].load(static_cast<const TA*>(a.rows) + int64_t(wv) * a.K + c * 8);
+        g[j].load(static_cast<const TA*>(a.gamma) + c * 8);
       }
     }
   }
   __device__ __forceinline__ void store(const I8Args& a, int lane, int wv, int8_t* codes, float* sx) {
+    if (wv >= a.T) return;
+    float v[NCH][8], ss = 0.f;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int t = wv + 8 * i;
-      if (t >= a.T) break;                   // uniform over the wave
-      float v[NCH][8], ss = 0.f;
+    for (int j = 0; j < NCH; ++j) {
+      if (j * 64 + lane < a.K / 8) {
+        x[j].get(v[j]);
+        float sj = v[j][0] * v[j][0];
 #pragma unroll
-      for (int j = 0; j < NCH; ++j) {
-        if (j * 64 + lane < a.K / 8) {
-          x[i][j].get(v[j]);
-          float sj = v[j][0] * v[j][0];
+        for (int e = 1; e < 8; ++e) sj = fmaf(v[j][e], v[j][e], sj);
+        ss += sj;
+      }
+    }
+    const float rinv = inv_rms(wave_sum(ss), a.K, a.eps);
+    float m = 0.f;
 #pragma unroll
-          for (int e = 1; e < 8; ++e) sj = fmaf(v[j][e], v[j][e], sj);
-          ss += sj;
+    for (int j = 0; j < NCH; ++j)
+      if (j * 64 + lane < a.K / 8) {
+        float gv[8];
+        g[j].get(gv);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          v[j][e] = v[j][e] * rinv * gv[e];
+          m = fmaxf(m, fabsf(v[j][e]));
         }
       }
-      const float rinv = inv_rms(wave_sum(ss), a.K, a.eps);
-      float m = 0.f;
+    const float scale = i8_scale(wave_max(m));
+    if (lane == 0) sx[wv] = scale;
+    const Divider by(scale);
 #pragma unroll
-      for (int j = 0; j < NCH; ++j)
-        if (j * 64 + lane < a.K / 8) {
-          float gv[8];
-          g[j].get(gv);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            v[j][e] = v[j][e] * rinv * gv[e];
-            m = fmaxf(m, fabsf(v[j][e]));
-          }
-        }
-      const float scale = i8_scale(wave_max(m));
-      if (lane == 0) sx[t] = scale;
-      const Divider by(scale);
-#pragma unroll
-      for (int j = 0; j < NCH; ++j) {
-        const int c = j * 64 + lane;
-        if (c < a.K / 8) *reinterpret_cast<uint2*>(codes + t * few_stride(a.K) + c * 8) = i8x8(v[j], by);
-      }
+    for (int j = 0; j < NCH; ++j) {
+      const int c = j * 64 + lane;
+      if (c < a.K / 8) *reinterpret_cast<uint2*>(codes + wv * few_stride(a.K) + c * 8) = i8x8(v[j], by);
     }
   }
 };
 
-// int8 codes of h in LDS: the 8 waves share the rows (all eight on one row, four on each of
-// two, two on each of four, one on each of eight, two rows each beyond).  A row's largest value
-// comes from its tiles' maxima, so h is read once; a lane's first chunks and maxima are on
-// their way before the weights.
+// int8 codes of up to eight rows of h in LDS: the 8 waves share the rows (all eight on one row,
+// four on each of two, two on each of four, one each beyond).  A row's largest value comes from
+// its tiles' maxima, so h is read once; a lane's first chunks and maxima are on their way before
+// the weights, the rest comes in groups, a round trip each.
 struct FewQuant {
-  static constexpr int WAVES = 4;
-  static constexpr int PRE = 2, HM = 6;
-  Chunk8<float> h[2][PRE];
-  float hm[2][HM];
-  int wpr;
-  __device__ __forceinline__ void load(const I8Args& a, int lane, int wv) {
-    wpr = a.T == 1 ? 8 : a.T == 2 ? 4 : a.T <= 4 ? 2 : 1;
-    const int nt = (a.K + 15) / 16;
+  static constexpr int PRE = 4, HM = 6;
+  Chunk8<float> h[PRE];
+  float hm[HM];
+  int wpr, t;
+  __device__ __forceinline__ void group(const I8Args& a, int c0) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int t = wv / wpr + 8 / wpr * i;
-      if (t >= a.T) break;                   // uniform over the wave
-#pragma unroll
-      for (int j = 0; j < HM; ++j)
-        hm[i][j] = a.hmax[int64_t(t) * nt + min(j * 64 + lane, nt - 1)];
-#pragma unroll
-      for (int j = 0; j < PRE; ++j) {
-        const int c = j * 64 * wpr + (wv % wpr) * 64 + lane;
-        if (c < a.K / 8) h[i][j].load(static_cast<const float*>(a.rows) + int64_t(t) * a.K + c * 8);
-      }
+    for (int j = 0; j < PRE; ++j) {
+      const int c = c0 + j * 64 * wpr;
+      if (c < a.K / 8) h[j].load(static_cast<const float*>(a.rows) + int64_t(t) * a.K + c * 8);
     }
   }
-  __device__ __forceinline__ void store(const I8Args& a, int lane, int wv, int8_t* codes, float* sx) {
+  __device__ __forceinline__ void load(const I8Args& a, int lane, int wv) {
+    wpr = a.T == 1 ? 8 : a.T == 2 ? 4 : a.T <= 4 ? 2 : 1;
+    t = wv / wpr;
+    if (t >= a.T) return;                    // uniform over the wave
     const int nt = (a.K + 15) / 16;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int t = wv / wpr + 8 / wpr * i;
-      if (t >= a.T) break;
-      float m = 0.f;
+    for (int j = 0; j < HM; ++j) hm[j] = a.hmax[int64_t(t) * nt + min(j * 64 + lane, nt - 1)];
+    group(a, (wv % wpr) * 64 + lane);
+  }
+  __device__ __forceinline__ void store(const I8Args& a, int lane, int wv, int8_t* codes, float* sx) {
+    if (t >= a.T) return;
+    const int nt = (a.K + 15) / 16;
+    float m = 0.f;
 #pragma unroll
-      for (int j = 0; j < HM; ++j) m = fmaxf(m, hm[i][j]);
-      for (int c = HM * 64 + lane; c < nt; c += 64) m = fmaxf(m, a.hmax[int64_t(t) * nt + c]);
-      const float scale = i8_scale(wave_max(m));
-      if (lane == 0) sx[t] = scale;          // (the waves of a row write the same value)
-      const Divider by(scale);
-      int8_t* const row = codes + t * few_stride(a.K);
+    for (int j = 0; j < HM; ++j) m = fmaxf(m, hm[j]);
+    for (int c = HM * 64 + lane; c < nt; c += 64) m = fmaxf(m, a.hmax[int64_t(t) * nt + c]);
+    const float scale = i8_scale(wave_max(m));
+    if (lane == 0) sx[t] = scale;            // (the waves of a row write the same value)
+    const Divider by(scale);
+    int8_t* const row = codes + t * few_stride(a.K);
+    const int step = PRE * 64 * wpr;
+    for (int c0 = (wv % wpr) * 64 + lane;;) {
 #pragma unroll
       for (int j = 0; j < PRE; ++j) {
-        const int c = j * 64 * wpr + (wv % wpr) * 64 + lane;
-        float v[8];
-        h[i][j].get(v);
-        if (c < a.K / 8) *reinterpret_cast<uint2*>(row + c * 8) = i8x8(v, by);
+        const int c = c0 + j * 64 * wpr;
+        if (c < a.K / 8) {
+          float v[8];
+          h[j].get(v);
+          *reinterpret_cast<uint2*>(row + c * 8) = i8x8(v, by);
+        }
       }
-      for (int c = PRE * 64 * wpr + (wv % wpr) * 64 + lane; c < a.K / 8; c += 64 * wpr) {
-        float v[8];
-        load8(static_cast<const float*>(a.rows) + int64_t(t) * a.K + c * 8, v);
-        *reinterpret_cast<uint2*>(row + c * 8) = i8x8(v, by);
-      }
+      c0 += step;
+      if (c0 - lane >= a.K / 8) break;       // uniform over the wave
+      group(a, c0);
     }
   }
 };
 struct FewNone {
-  static constexpr int WAVES = 4;
   __device__ __forceinline__ void load(const I8Args&, int, int) {}
   __device__ __forceinline__ void store(const I8Args&, int, int, int8_t*, float*) {}
 };
@@ -205,12 +194,14 @@ struct FewNone {
 // 16x16x64 step (which k an MFMA slot stands for is free as long as both operands agree), so a
 // row's unit is one 128-byte line.  Two units per wave are in flight while codes are made and
 // beside the two in use.
-// T <= 16 TB; grid = ceil(N / 16), block = 512, dynamic LDS = T * few_stride(K) unless kCodes.
+// T <= 16 TB (<= 8 unless kCodes); grid = ceil(N / 16), block = 512, dynamic LDS = T *
+// few_stride(K) unless kCodes.  At most 128 registers, so that two workgroups share a CU: a grid is
+// often a little over one per CU.
 template <typename TO, int TB, bool GLU, FewSrc SRC, class Make>
-__global__ __launch_bounds__(512, Make::WAVES) void k_i8_few(I8Args a) {
+__global__ __launch_bounds__(512, 4) void k_i8_few(I8Args a) {
   constexpr int NW = 8, NA = GLU ? 2 : 1;
   __shared__ i32x4 part[NW][NA * TB][64];
-  __shared__ float own_sx[16];
+  __shared__ float own_sx[8];
   extern __shared__ __align__(16) int8_t own_codes[];
   const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
   const int r16 = lane & 15, q = lane >> 4;
@@ -273,13 +264,19 @@ __global__ __launch_bounds__(512, Make::WAVES) void k_i8_few(I8Args a) {
   auto load_end = [&] {
     if (wv >= TB) return;
     if (SRC == kCodes) est = a.sx[min(ot, T - 1)];
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
+    const TO* const res = GLU ? nullptr : static_cast<const TO*>(a.res);
+    const int64_t rrow = int64_t(min(ot, T - 1)) * N;
+    // (four statements: as a loop the arrays went to scratch memory for fp32 outputs)
+    auto column = [&](int r, float& s0, float& s1, float& e) {
       const int nr = min(on + r, N - 1);
-      es0[r] = a.sw[nr];
-      if (GLU) es1[r] = a.su[nr];
-      if (a.res) er[r] = to_f32<TO>(static_cast<const TO*>(a.res)[int64_t(min(ot, T - 1)) * N + nr]);
-    }
+      s0 = a.sw[nr];
+      if (GLU) s1 = a.su[nr];
+      if (res) e = to_f32<TO>(res[rrow + nr]);
+    };
+    column(0, es0[0], es1[0], er[0]);
+    column(1, es0[1], es1[1], er[1]);
+    column(2, es0[2], es1[2], er[2]);
+    column(3, es0[3], es1[3], er[3]);
   };
   Unit f0, f1;
   int u = wv;
@@ -346,13 +343,15 @@ __global__ __launch_bounds__(512, Make::WAVES) void k_i8_few(I8Args a) {
     if (q == 0 && t < T) a.hmax[int64_t(t) * gridDim.x + blockIdx.x] = m;
   }
   if (t < T)
-    store_out4<TO>(static_cast<TO*>(a.y), int64_t(t) * N, n, N, a.vec, v);
+    store_out4<TO>(static_cast<TO*>(a.y), int64_t(t) * N, n, N, a.vec,
+                   make_float4(v[0], v[1], v[2], v[3]));
 }
 
 // 16-byte chunks of the tile's LDS rows are XOR-swizzled so that the 16 consecutive rows one
 // ds_read_b128 serves together at one chunk lie in 16 different 16-byte slots of a bank line.
 template <int BK> __device__ __forceinline__ int i8_swz(int row) {
-  return BK == 64 ? (row >> 2) & 3 : BK == 128 ? (row >> 1) & 7 : row & 15;
+  static_assert(BK == 128 || BK == 256, "a row is half a bank line or a whole one");
+  return BK == 128 ? (row >> 1) & 7 : row & 15;
 }
 
 // Tile of a workgroup: workgroup b runs on XCD b % 8, every XCD takes one contiguous run
@@ -945,11 +944,13 @@ int launch_i8_product(const I8Product& p, hipStream_t st) {
   return p.w_up ? launch_product<bf16_t, true>(p, st) : launch_product<bf16_t, false>(p, st);
 }
 
-// The dense layer of up to 16 tokens in two launches: norm, codes and gated product; codes of
+// The dense layer of up to 8 tokens in two launches: norm, codes and gated product; codes of
 // h, down product and residual.  Every workgroup makes the codes it needs (a few rows, from L2)
-// while its first weights are on their way, which costs less than a launch between the stages.
+// while its first weights are on their way.  Against the four launches (us, bf16, 1536 x 5120):
+// 1 token 13.1 / 16.6, 4 tokens 14.4 / 17.1, 8 tokens 17.0 / 17.9; with two rows per wave 16 tokens
+// took 22.4 / 19.1, and wider rows (4 tokens, 4096 x 8192) 33.7 / 30.7: those take the four.
 bool dense_few_ok(int64_t T, int H, int I) {
-  return T <= 16 && H <= 4096 && T * few_stride(H) <= kFewCodes && T * few_stride(I) <= kFewCodes;
+  return T <= 8 && H <= 2048 && T * few_stride(H) <= kFewCodes && T * few_stride(I) <= kFewCodes;
 }
 size_t dense_few_hmax_bytes(int64_t T, int I) { return size_t(T) * ((I + 15) / 16) * sizeof(float); }
 
@@ -961,10 +962,7 @@ static int launch_dense_few_act(const DenseFew& d, hipStream_t st) {
   up.rows = d.x; up.gamma = d.gamma; up.eps = d.eps; up.hmax = d.hmax;
   const dim3 gu(unsigned((d.I + 15) / 16)), gd(unsigned((d.H + 15) / 16));
   const size_t lu = size_t(d.T) * few_stride(d.H), ld = size_t(d.T) * few_stride(d.I);
-  if (d.H <= 2048)
-    hipLaunchKernelGGL((k_i8_few<float, 1, true, kNorm, FewNorm<TA, 4>>), gu, dim3(512), lu, st, up);
-  else
-    hipLaunchKernelGGL((k_i8_few<float, 1, true, kNorm, FewNorm<TA, 8>>), gu, dim3(512), lu, st, up);
+  hipLaunchKernelGGL((k_i8_few<float, 1, true, kNorm, FewNorm<TA>>), gu, dim3(512), lu, st, up);
   MOE_TRY(check_launch());
   I8Args down{};
   down.w = d.w->w_down; down.sw = d.w->s_down; down.res = d.x; down.y = d.x_out;
