@@ -333,7 +333,9 @@ int moe_forward_paged(const moe_config* cfg, const void* x, const moe_weights* h
  * residual NULL the call quantises (MOE_ROWS_I8 over [out, in] weights gives the codes and
  * channel scales the products below take).
  * The sum of squares is fp32: it has to stay finite, and squares below its range count as zero; a
- * row of which nothing is left (with norm_eps 0 too) gives zeros.
+ * row of which nothing is left (with norm_eps 0 too) gives zeros.  A row (block) of v with a NaN
+ * or an infinity gets the scale NaN or infinity (E8M0 code 255) and unspecified codes, so that
+ * what is computed from it is not finite either; other rows (blocks) do not change.
  * act_dtype MOE_F32 or MOE_BF16; width a multiple of 8 (128 for E4M3_B128, 32 for MXFP8), at
  * most 32768; rows <= 2^21.  x_sum (required with a residual, else ignored) may be x or
  * residual, and a MOE_ROWS_ACT out may be x or residual; other overlaps are not allowed.
@@ -374,7 +376,8 @@ int moe_glu_i8(int64_t rows, int32_t in_width, int32_t out_width, int32_t out_dt
  *   x_out = round(x + down(i8(glu(i8(RMSNorm(x) * norm_weight)))))
  * with i8() the per-token quantisation of moe_norm_quant_rows; h is not rounded to act_dtype
  * between the products (it is held in fp32, or in 16 bits with a scale per row and 32 columns,
- * 0.002 of a step of its codes apart from that).  x, x_out [T, H] act_dtype; x_out may be x
+ * 0.002 of a step of its codes apart from that).  A row with a NaN or an infinity gives a row
+ * without finite values; other rows do not change.  x, x_out [T, H] act_dtype; x_out may be x
  * itself.  hidden and intermediate are multiples of 16, at most 32768, T <= 2^21 and T times
  * either at most 2^35.  ws: moe_dense_workspace_size() bytes,
  * 256-byte aligned.

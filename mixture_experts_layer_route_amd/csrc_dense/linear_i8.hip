@@ -114,10 +114,10 @@ struct FewNorm {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           v[j][e] = v[j][e] * rinv * gv[e];
-          m = fmaxf(m, fabsf(v[j][e]));
+          m = nmax(m, fabsf(v[j][e]));
         }
       }
-    const float scale = i8_scale(wave_max(m));
+    const float scale = i8_scale(wave_nmax(m));
     if (lane == 0) sx[wv] = scale;
     const Divider by(scale);
 #pragma unroll
@@ -158,9 +158,9 @@ struct FewQuant {
     const int nt = (a.K + 15) / 16;
     float m = 0.f;
 #pragma unroll
-    for (int j = 0; j < HM; ++j) m = fmaxf(m, hm[j]);
-    for (int c = HM * 64 + lane; c < nt; c += 64) m = fmaxf(m, a.hmax[int64_t(t) * nt + c]);
-    const float scale = i8_scale(wave_max(m));
+    for (int j = 0; j < HM; ++j) m = nmax(m, hm[j]);
+    for (int c = HM * 64 + lane; c < nt; c += 64) m = nmax(m, a.hmax[int64_t(t) * nt + c]);
+    const float scale = i8_scale(wave_nmax(m));
     if (lane == 0) sx[t] = scale;            // (the waves of a row write the same value)
     const Divider by(scale);
     int8_t* const row = codes + t * few_stride(a.K);
@@ -337,9 +337,9 @@ __global__ __launch_bounds__(512, 4) void k_i8_few(I8Args a) {
     float m = 0.f;
 #pragma unroll
     for (int r = 0; r < 4; ++r)
-      if (n + r < N) m = fmaxf(m, fabsf(v[r]));
-    m = fmaxf(m, __shfl_xor(m, 16));
-    m = fmaxf(m, __shfl_xor(m, 32));
+      if (n + r < N) m = nmax(m, fabsf(v[r]));
+    m = nmax(m, __shfl_xor(m, 16));
+    m = nmax(m, __shfl_xor(m, 32));
     if (q == 0 && t < T) a.hmax[int64_t(t) * gridDim.x + blockIdx.x] = m;
   }
   if (t < T)
@@ -441,10 +441,10 @@ __device__ __forceinline__ void i8_epilogue(unsigned char* stg, const i32x4 (&ac
         for (int f = 0; f < FO; ++f)
           if (nw + f * 16 < N) {                         // (N is a multiple of 16 here)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) mx = fmaxf(mx, fabsf(v[f][r]));
+            for (int r = 0; r < 4; ++r) mx = nmax(mx, fabsf(v[f][r]));
           }
-        mx = fmaxf(mx, __shfl_xor(mx, 16));
-        mx = fmaxf(mx, __shfl_xor(mx, 32));
+        mx = nmax(mx, __shfl_xor(mx, 16));
+        mx = nmax(mx, __shfl_xor(mx, 32));
         const int64_t t = tw + m * 16 + l16;
         if (q == 0 && t < T && nw < N) a.hmax[t * ((N + 31) / 32) + nw / 32] = mx;
         const float up = mx >= 1.17549435e-38f ? 32767.0f / mx : 0.0f;
@@ -904,11 +904,11 @@ __global__ __launch_bounds__(256) void k_h16_codes(const int16_t* h, const float
     m32[j] = gm[k / 4];
   }
   float m = 0.f;
-  for (int g = tid; g < ng; g += 256) m = fmaxf(m, gm[g]);
-  m = wave_max(m);
+  for (int g = tid; g < ng; g += 256) m = nmax(m, gm[g]);
+  m = wave_nmax(m);
   if ((tid & 63) == 0) part[tid >> 6] = m;
   __syncthreads();
-  m = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
+  m = nmax(nmax(part[0], part[1]), nmax(part[2], part[3]));
   const float scale = i8_scale(m);
   if (tid == 0) scales[t] = scale;
   const float step = 1.0f / (32767.0f * scale);     // codes of h16 -> codes, times the group's maximum

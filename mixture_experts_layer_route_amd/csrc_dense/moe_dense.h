@@ -73,18 +73,28 @@ int launch_dense_few(const DenseFew& d, hipStream_t st);
 // every code of the row).  A row without squares and without eps is left as it is, at zero.
 __device__ __forceinline__ float inv_rms(float sum_sq, int width, float eps) {
   const double ms = double(sum_sq) / width + double(eps);
-  return ms > 0.0 ? float(1.0 / sqrt(ms)) : 0.0f;
+  return ms == 0.0 ? 0.0f : float(1.0 / sqrt(ms));
+}
+// Maximum that keeps a NaN (one v_maximum3_f32 for two of them): 8-bit codes cannot hold one, so
+// a row's or block's scale carries it on to whatever reads the codes.
+__device__ __forceinline__ float nmax(float a, float b) { return __builtin_elementwise_maximum(a, b); }
+__device__ __forceinline__ float wave_nmax(float v) {
+  v = nmax(v, dppf<0xB1>(v));
+  v = nmax(v, dppf<0x4E>(v));
+  v = nmax(v, dppf<0x141>(v));
+  v = nmax(v, dppf<0x140>(v));
+  return nmax(nmax(lanef(v, 0), lanef(v, 16)), nmax(lanef(v, 32), lanef(v, 48)));
 }
 // Per-row int8: scale = amax / 127.  A row whose amax is so small that the scale would leave
 // the normal floats (or is zero) has scale 1 and codes 0, so no division overflows.
 __device__ __forceinline__ float i8_scale(float amax) {
   const float s = amax / 127.0f;
-  return s >= 1.17549435e-38f ? s : 1.0f;
+  return s < 1.17549435e-38f ? 1.0f : s;
 }
 // the block-FP8 rule of quant_e4m3_wave with the same guard
 __device__ __forceinline__ float e4m3_scale(float amax) {
   const float s = amax / 448.0f;
-  return s >= 1.17549435e-38f ? s : 1.0f;
+  return s < 1.17549435e-38f ? 1.0f : s;
 }
 // v / scale for many values of one scale: the product with the reciprocal and one correction
 // step, within an ulp of the quotient, in three operations where the division sequence takes

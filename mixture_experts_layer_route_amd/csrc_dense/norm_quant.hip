@@ -100,14 +100,14 @@ __global__ __launch_bounds__(WPR == 16 ? 1024 : 256) void k_norm_quant(NormQuant
 #pragma unroll
     for (int j = 0; j < NCH; ++j)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[j][i]));
-    m = wave_max(m);
+      for (int i = 0; i < 8; ++i) m = nmax(m, fabsf(v[j][i]));
+    m = wave_nmax(m);
     if (WPR > 1) {
       if (lane == 0) part[NW + wv] = m;
       __syncthreads();
       m = 0.f;
 #pragma unroll
-      for (int i = 0; i < WPR; ++i) m = fmaxf(m, part[NW + wv / WPR * WPR + i]);
+      for (int i = 0; i < WPR; ++i) m = nmax(m, part[NW + wv / WPR * WPR + i]);
     }
     row_scale = i8_scale(m);
     if (pos == 0) static_cast<float*>(scales)[t] = row_scale;
@@ -126,13 +126,13 @@ __global__ __launch_bounds__(WPR == 16 ? 1024 : 256) void k_norm_quant(NormQuant
     } else {
       float m = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[j][i]));
-      m = fmaxf(m, dppf<0xB1>(m));    // quad_perm [1,0,3,2]
-      m = fmaxf(m, dppf<0x4E>(m));    // quad_perm [2,3,0,1]
+      for (int i = 0; i < 8; ++i) m = nmax(m, fabsf(v[j][i]));
+      m = nmax(m, dppf<0xB1>(m));    // quad_perm [1,0,3,2]
+      m = nmax(m, dppf<0x4E>(m));    // quad_perm [2,3,0,1]
       uint32_t c0, c1;
       if (FMT == MOE_ROWS_E4M3_B128) {
-        m = fmaxf(m, dppf<0x141>(m));   // row_half_mirror
-        m = fmaxf(m, dppf<0x140>(m));   // row_mirror
+        m = nmax(m, dppf<0x141>(m));   // row_half_mirror
+        m = nmax(m, dppf<0x140>(m));   // row_mirror
         const float s = e4m3_scale(m);
         const Divider by(s);
         c0 = e4m3x4(by(v[j][0]), by(v[j][1]), by(v[j][2]), by(v[j][3]));
@@ -144,7 +144,7 @@ __global__ __launch_bounds__(WPR == 16 ? 1024 : 256) void k_norm_quant(NormQuant
         c0 = e4m3x4(v[j][0] * inv, v[j][1] * inv, v[j][2] * inv, v[j][3] * inv);
         c1 = e4m3x4(v[j][4] * inv, v[j][5] * inv, v[j][6] * inv, v[j][7] * inv);
         if (live && (lane & 3) == 0)
-          static_cast<uint8_t*>(scales)[t * (H / 32) + c / 4] = uint8_t(X + 127);
+          static_cast<uint8_t*>(scales)[t * (H / 32) + c / 4] = m < INFINITY ? uint8_t(X + 127) : 255;
       }
       if (live) *reinterpret_cast<uint2*>(static_cast<uint8_t*>(out) + off) = make_uint2(c0, c1);
     }

@@ -28,10 +28,11 @@ def norm_rows(x, gamma=None, residual=None, eps=mo.RMS_EPS, act="bf16") -> np.nd
 
 
 def quant_i8(v):
-    """(codes, scales): scale = amax / 127 per row (1 for a zero row), code = rint(v / scale)."""
+    """(codes, scales): scale = amax / 127 per row (1 for a zero row, not finite where the row is
+    not), code = rint(v / scale)."""
     v = np.asarray(v, dtype=np.float64)
     amax = np.abs(v).max(axis=1)
-    scale = np.where(amax > 0, amax / 127.0, 1.0)
+    scale = np.where(amax == 0, 1.0, amax / 127.0)
     return np.clip(np.rint(v / scale[:, None]), -127, 127), scale
 
 

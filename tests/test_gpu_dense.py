@@ -154,6 +154,39 @@ def test_norm_zero_tiny_and_huge_rows(moe, fmt):
     check_rows(out, scales, fmt, np.stack([v[0], mo.rms_norm(v[1], np.ones(H), 0.0)]), torch.float32)
 
 
+@pytest.mark.parametrize("T,H", [(7, 512), (7, 2048), (2050, 1024), (5, 8192), (3, 16384)])
+@pytest.mark.parametrize("fmt", list(WIDTHS))
+def test_norm_rows_that_are_not_finite(moe, fmt, T, H):
+    """A NaN, an infinity, a NaN in the residual: the row's scale (with the norm every block's, for
+    an infinity at least its own block's) is not finite; the other rows keep their bits."""
+    print("case: not finite", fmt, T, H, flush=True)
+    g = gen(H)
+    x, r = torch.randn(T, H, generator=g, device="cuda"), torch.randn(T, H, generator=g, device="cuda")
+    gamma = torch.ones(H, device="cuda")
+    bx, br = x.clone(), r.clone()
+    bx[0, 5], bx[1, H - 1], br[2, H // 2] = float("nan"), float("inf"), float("nan")
+    n = {"rows": 1, "i8": H, "e4m3": 128, "mxfp8": 32}[fmt]
+    for w, hit in ((gamma, (True, False, True)), (None, (False, False, False))):
+        out, sc, _ = moe.norm_quant_rows(x, fmt, w, r)
+        bad, bsc, _ = moe.norm_quant_rows(bx, fmt, w, br)
+        assert torch.equal(out[3:], bad[3:]) and (sc is None or torch.equal(sc[3:], bsc[3:]))
+        if fmt == "rows":
+            lost = ~torch.isfinite(bad[:3])
+        elif fmt == "mxfp8":
+            lost = bsc[:3] == 255
+        else:
+            lost = ~torch.isfinite(bsc[:3].reshape(3, -1))
+        for t, at in enumerate((5, H - 1, H // 2)):
+            assert lost[t, at // n]
+            assert not hit[t] or lost[t].all()
+            assert w is not None or lost[t].sum() == 1
+    # quantised alone, zeros beside one infinity: nothing else is touched
+    z = torch.zeros(T, H, device="cuda")
+    z[1, 0] = float("-inf")
+    out, sc, _ = moe.norm_quant_rows(z, fmt)
+    assert (out[0].float() == 0).all() and (out[2:].float() == 0).all()
+
+
 def test_norm_in_place_and_neighbours(moe):
     """x_sum may be x or the residual and a rows output x; nothing behind the rows changes."""
     T, H = 9, 1544
@@ -380,6 +413,33 @@ def test_dense_layer(moe, T, H, I, act):
     assert tol <= 0.1 * size
     moe.dense_residual_i8(cfg, x, gamma, wst, ws, x_out=x)   # in place, the same bits
     assert torch.equal(x, got)
+
+
+@pytest.mark.parametrize("T,H,I", [(3, 1536, 1040), (16, 2064, 1040), (90, 512, 784), (700, 1536, 1040),
+                                   (4100, 2048, 2064)])
+def test_layer_rows_that_are_not_finite(moe, T, H, I):
+    """A NaN in one row, an infinity in another: no value of those rows is finite, the others keep
+    their bits; then a scale that takes h of every row beyond fp32."""
+    print("case: layer, not finite", T, H, I, flush=True)
+    g = gen(T + 11)
+    w, gamma = layer(g, H, I, "bf16")
+    x = torch.randn(T, H, generator=g, device="cuda").to(torch.bfloat16)
+    bad = x.clone()
+    bad[0, H - 1], bad[T - 1, 0] = float("nan"), float("-inf")
+    cfg = moe.make_dense_config(T, H, I)
+    ws, wst = moe.alloc_dense_workspace(cfg), moe.dense_weights_struct(w)
+    good, got = (moe.dense_residual_i8(cfg, v, gamma, wst, ws) for v in (x, bad))
+    assert torch.equal(good[1:T - 1], got[1:T - 1])
+    assert not torch.isfinite(got[0]).any() and not torch.isfinite(got[T - 1]).any()
+    w["s_up"][I - 1], w["s_gate"][I - 1] = 1e38, 1.0
+    got = moe.dense_residual_i8(cfg, x, gamma, wst, ws)
+    acc = f64(moe.linear_i8(*moe.norm_quant_rows(x, "i8", gamma)[:2], w["w_gate"][I - 1:],
+                            torch.ones(1, device="cuda"), torch.float32))[:, 0]
+    up = f64(moe.linear_i8(*moe.norm_quant_rows(x, "i8", gamma)[:2], w["w_up"][I - 1:],
+                           torch.ones(1, device="cuda"), torch.float32))[:, 0]
+    over = (acc > 100) & (np.abs(up) > 10)                # silu(g) |u| 1e38 is far beyond fp32
+    print("rows beyond fp32:", over.sum(), "of", T, flush=True)
+    assert not torch.isfinite(got[torch.from_numpy(over).cuda()]).any()
 
 
 @pytest.mark.parametrize("T", [64, 700])
