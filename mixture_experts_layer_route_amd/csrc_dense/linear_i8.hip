@@ -67,8 +67,6 @@ struct h16_t { int16_t code; };
 // itself in LDS, from activation rows (RMSNorm in front) or from the fp32 h of the gated product.
 enum FewSrc { kCodes, kNorm, kQuant };
 
-constexpr int kFewCodes = 128 << 10;     // LDS bytes of codes a workgroup may make
-
 // LDS row stride of the codes: 16 tokens' equal chunks fall on 16 different bank groups
 // (a row is a whole number of 256-byte bank lines for the usual widths).
 __host__ __device__ inline int few_stride(int K) { return (K + 255) / 256 * 256 + 16; }
@@ -819,29 +817,34 @@ using Tile128 = I8Tile<128, 128, 4, 2, 128, 3>;
 using Tile64Deep = I8Tile<64, 64, 1, 2, 256, 3, 4>;
 using Tile64 = I8Tile<64, 64, 2, 2, 128, 3, 2>;
 using Tile32 = I8Tile<32, 64, 1, 2, 256, 3, 4>;
+using Tile32Narrow = I8Tile<32, 32, 1, 1, 256, 3, 4>;
 
-// Which kernel: up to 16 tokens (32 without the gate) the weights are streamed past every
-// token at once; beyond, the tile whose estimated time is least.  The estimate is
+// Which kernel: the one whose estimated time (us) is least.  For a tile that is
 //   (128-wide K slabs) * (tiles on the fullest CU) * (time of a slab) + (start and end),
-// fitted to measurements from 64 to 8192 tokens and widths from 1040 to 8192 (us a slab: 0.19,
-// 0.26, 0.56 alone and 0.65 among others for 32x64, 64x64, 128x128; start and end 2.8, 3.3, 3.7;
-// the deep 64x64 tile 0.20 and 3.9, where every tile has a CU of its own; a round of 256x256
-// tiles 1.6 and 4).
-// Measured on either side of a switch (us): 64 x 1536 x 4096 few 5.9, 32x64 5.1, 64x64 6.4;
-// 200 x 1536 x 1536 32x64 5.1, deep 6.1; 512 x 2048 x 2048 32x64 8.8, 64x64 8.4, deep 7.7, 128x128
-// 12.3; 2048 x 2048 x 2048 64x64 18.3, deep 25.5, 128x128 14.1; 8192 x 8192 x 2048 128x128 148,
-// 256x256 109; gated 333 x 1536 x 4112 64x64 14.1, 128x128 11.1.
-enum I8Kernel { kFew16, kFew32, kTile32, kTile64, kTile64Deep, kTile128, kTile256 };
+// and at least the weight stream from memory, fitted to measurements from 1 to 8192
+// tokens and widths from 512 to 32768.  Up to 16 tokens (32 without the gate) there is also the
+// kernel that streams the weights past every token at once: a time per MB of weights and one per
+// token for the codes that each workgroup reads for itself, on at least 256 CUs, the last round
+// of workgroups counted half; widths up to 2048 have all their weights on the way from the start.
+// Measured on either side of a switch (us; few rows / narrow 32x32 / 32x64): 1 x 2048 x 16384
+// 7.5 / 8.0 / 7.9; 4 x 4096 x 16384 14.3 / 12.3 / 12.3; 16 x 2048 x 2048 4.2 / 5.2; 16 x 8192 x
+// 8192 16.8 / 12.6 / 13.4; 16 x 1536 x 32768 13.1 / 11.6 / 10.3; 17 x 5120 x 1536 7.1 / 8.4 / 9.0;
+// 32 x 5120 x 1536 8.9 / 8.4 / 9.0; 32 x 4096 x 16384 23.5 / 12.7 / 12.8; gated 4 x 1536 x 5120 6.4 /
+// 6.2 / 5.9, 16 x 2048 x 1024 4.9 / 5.1 / 5.5.  64 x 5120 x 1536 narrow 8.6, 32x64 9.3, 64x64 14.4;
+// 64 x 4096 x 8192 9.8, 8.8, 12.3; 48 x 2048 x 16384 11.1, 9.0, 8.4; 333 x 4112 x 1536 14.1, 14.3,
+// 13.2, deep 12.2; 512 x 2048 x 2048 32x64 8.9, 64x64 8.4, deep 8.2, 128x128 13.0; 2048 x 2048 x 2048
+// 64x64 18.3, deep 25.5, 128x128 14.1; 8192 x 8192 x 2048 128x128 148, 256x256 109; gated 333 x
+// 1536 x 4112 64x64 14.7, 128x128 11.2.
+enum I8Kernel { kFew16, kFew32, kTile32Narrow, kTile32, kTile64, kTile64Deep, kTile128, kTile256 };
 static I8Kernel pick_kernel(int64_t T, int K, int N, bool glu) {
-  if (T <= 16) return kFew16;
-  if (T <= 32 && !glu) return kFew32;
-  const double slabs = double((K + 127) / 128);
+  const double slabs = double((K + 127) / 128), mats = glu ? 2.0 : 1.0;
+  const double mb = mats * K * N * 1e-6;                     // of weights
   auto per_cu = [&](int bm, int bn) {
     const int oc = glu ? bn / 2 : bn;
     return std::ceil(double((T + bm - 1) / bm) * double((N + oc - 1) / oc) / 256.0);
   };
-  const double c64 = per_cu(64, 64), c128 = per_cu(128, 128);
-  double least = slabs * per_cu(32, 64) * 0.19 + 2.8;
+  const double c32 = per_cu(32, 64), c64 = per_cu(64, 64), c128 = per_cu(128, 128);
+  double least = std::max(slabs * c32 * (c32 == 1.0 ? 0.16 : 0.19) + 2.85, mb * 0.14 + 3.2);
   I8Kernel pick = kTile32;
   auto offer = [&](I8Kernel k, double us) {
     if (us < least) {
@@ -849,10 +852,18 @@ static I8Kernel pick_kernel(int64_t T, int K, int N, bool glu) {
       pick = k;
     }
   };
-  offer(kTile64, slabs * c64 * 0.26 + 3.3);
-  if (c64 == 1.0) offer(kTile64Deep, slabs * 0.20 + 3.9);
+  if (per_cu(32, 32) == 1.0) offer(kTile32Narrow, std::max(slabs * 0.145 + 2.85, mb * 0.144 + 3.2));
+  offer(kTile64, std::max(slabs * c64 * 0.26 + 3.3, mb * 0.14 + 3.6));
+  if (c64 == 1.0) offer(kTile64Deep, std::max(slabs * 0.20 + 3.9, mb * 0.14 + 4.0));
   offer(kTile128, slabs * (c128 == 1.0 ? 0.56 : c128 * 0.65) + 3.7);
   offer(kTile256, per_cu(256, 256) * (slabs * 1.6 + 4.0));
+  if (T <= 16 || (T <= 32 && !glu)) {
+    const double wgs = (N + 15) / 16, rounds = std::ceil(wgs / 256.0) * 256.0;
+    const double stream = 16e-6 * mats * K * (wgs <= 256.0 ? 256.0 : (wgs + rounds) / 2);
+    const double start = wgs <= 256.0 && K <= 2048 ? 2.0 : 2.6;
+    if (T <= 16) offer(kFew16, stream * (0.152 + 0.0034 * T / mats) + start);
+    else offer(kFew32, stream * (0.145 + 0.0053 * T) + start);
+  }
   return pick;
 }
 // (a wave of these two tiles has the 32 columns of a group)
@@ -868,6 +879,7 @@ static int launch_product(const I8Product& p, hipStream_t st) {
     case kFew32:
       if constexpr (!GLU) launch_few<TO, GLU, 2>(p, st);
       break;
+    case kTile32Narrow: launch_tile<TO, GLU, Tile32Narrow>(p, st); break;
     case kTile32: launch_tile<TO, GLU, Tile32>(p, st); break;
     case kTile64: launch_tile<TO, GLU, Tile64>(p, st); break;
     case kTile64Deep: launch_tile<TO, GLU, Tile64Deep>(p, st); break;
@@ -946,11 +958,15 @@ int launch_i8_product(const I8Product& p, hipStream_t st) {
 
 // The dense layer of up to 8 tokens in two launches: norm, codes and gated product; codes of
 // h, down product and residual.  Every workgroup makes the codes it needs (a few rows, from L2)
-// while its first weights are on their way.  Against the four launches (us, bf16, 1536 x 5120):
-// 1 token 13.1 / 16.6, 4 tokens 14.4 / 17.1, 8 tokens 17.0 / 17.9; with two rows per wave 16 tokens
-// took 22.4 / 19.1, and wider rows (4 tokens, 4096 x 8192) 33.7 / 30.7: those take the four.
+// while its first weights are on their way, as long as a wave has one row to normalise and a lane at
+// most eight chunks of h (FewQuant's sharing).  Against the four launches (us, bf16,
+// hidden x intermediate): 1536 x 5120 1 token 13.6 / 16.0, 4 tokens 15.1 / 16.9, 5 tokens (10
+// chunks) 17.3 / 17.0; 2048 x 4096 8 tokens 15.5 / 16.2; 2048 x 8192 4 tokens 19.0 / 21.0, 5 tokens
+// 22.9 / 21.3; 2048 x 16384 4 tokens 37.9 / 33.2; with 4096 x 8192 and two rows' registers per wave 4
+// tokens took 33.7 / 30.7.
 bool dense_few_ok(int64_t T, int H, int I) {
-  return T <= 8 && H <= 2048 && T * few_stride(H) <= kFewCodes && T * few_stride(I) <= kFewCodes;
+  const int rows = T == 1 ? 1 : T == 2 ? 2 : T <= 4 ? 4 : 8;
+  return T <= 8 && H <= 2048 && rows * I <= 8 * 8 * 64 * 8;
 }
 size_t dense_few_hmax_bytes(int64_t T, int I) { return size_t(T) * ((I + 15) / 16) * sizeof(float); }
 

@@ -226,7 +226,9 @@ SHAPES = [(1, 16, 1), (1, 1536, 4096), (2, 48, 17), (4, 128, 33), (15, 144, 100)
           (100, 16, 256), (128, 128, 128), (129, 64, 129), (200, 2064, 384), (255, 80, 257),
           (300, 96, 1000), (513, 1536, 520), (513, 2064, 2041),
           (505, 2064, 1999), (1000, 208, 2000), (1025, 512, 2049), (2500, 4096, 1000),
-          (8100, 4112, 2041), (7937, 8192, 2048)]
+          (8100, 4112, 2041), (7937, 8192, 2048),
+          (16, 1536, 5120), (9, 4112, 8200), (20, 1040, 5001), (32, 4112, 16392), (32, 5136, 1541),
+          (5, 4096, 16385), (1, 2064, 32776), (1, 4096, 16384), (64, 5120, 1536), (40, 64, 8199)]
 
 
 @pytest.mark.parametrize("T,K,N", SHAPES)
@@ -249,7 +251,9 @@ def test_linear_i8(moe, T, K, N):
 @pytest.mark.parametrize("T,K,N", [(1, 1536, 5120), (4, 48, 33), (16, 2048, 64), (31, 1040, 130),
                                    (64, 272, 48), (100, 1536, 200), (130, 64, 129), (333, 1536, 1040), (333, 1552, 4107),
                                    (1025, 400, 2056), (2500, 2048, 1000),
-                                   (8100, 2064, 1021), (7937, 4096, 1024)])
+                                   (8100, 2064, 1021), (7937, 4096, 1024),
+                                   (16, 1536, 5119), (3, 1040, 16392), (1, 4112, 8200), (33, 1536, 2560),
+                                   (32, 2064, 1030), (9, 144, 4090)])
 def test_glu_i8(moe, T, K, N):
     for out in ("bf16", "f32"):
         print("case: glu", T, K, N, out, flush=True)
@@ -390,7 +394,8 @@ def layer_and_bound(x, gamma, w, act):
                                        (16, 1536, 5120, "bf16"), (15, 1024, 8192, "f32"), (3, 4096, 32768, "bf16"),
                                        (4090, 2048, 8176, "bf16"), (7900, 2048, 4112, "f32"),
                                        (8, 1536, 8192, "bf16"), (7, 2048, 16384, "f32"), (1, 3488, 4368, "bf16"),
-                                       (8, 2048, 80, "f32"), (5, 1488, 112, "bf16")])
+                                       (8, 2048, 80, "f32"), (5, 1488, 112, "bf16"), (1, 2048, 32768, "bf16"),
+                                       (8, 2048, 4096, "f32"), (2, 1024, 16384, "bf16"), (3, 512, 8192, "f32")])
 def test_dense_layer(moe, T, H, I, act):
     """x_out against the oracle run through all four stages, within layer_and_bound."""
     print("case: layer", T, H, I, act, flush=True)
