@@ -820,7 +820,8 @@ using Tile32 = I8Tile<32, 64, 1, 2, 256, 3, 4>;
 using Tile32Narrow = I8Tile<32, 32, 1, 1, 256, 3, 4>;
 
 // Which kernel: the one whose estimated time (us) is least.  For a tile that is
-//   (128-wide K slabs) * (tiles on the fullest CU) * (time of a slab) + (start and end),
+//   (128-wide K slabs) * (tiles on the fullest CU) * (time of a slab) + (start and end) +
+//   (the ends of a CU's further tiles, as far as they show),
 // and at least the weight stream from memory, fitted to measurements from 1 to 8192
 // tokens and widths from 512 to 32768.  Up to 16 tokens (32 without the gate) there is also the
 // kernel that streams the weights past every token at once: a time per MB of weights and one per
@@ -834,7 +835,7 @@ using Tile32Narrow = I8Tile<32, 32, 1, 1, 256, 3, 4>;
 // 64 x 4096 x 8192 9.8, 8.8, 12.3; 48 x 2048 x 16384 11.1, 9.0, 8.4; 333 x 4112 x 1536 14.1, 14.3,
 // 13.2, deep 12.2; 512 x 2048 x 2048 32x64 8.9, 64x64 8.4, deep 8.2, 128x128 13.0; 2048 x 2048 x 2048
 // 64x64 18.3, deep 25.5, 128x128 14.1; 8192 x 8192 x 2048 128x128 148, 256x256 109; gated 333 x
-// 1536 x 4112 64x64 14.7, 128x128 11.2.
+// 1536 x 4112 64x64 14.7, 128x128 11.2, 1485 x 288 x 13584 64x64 47.0, 128x128 47.6, 256x256 36.7.
 enum I8Kernel { kFew16, kFew32, kTile32Narrow, kTile32, kTile64, kTile64Deep, kTile128, kTile256 };
 static I8Kernel pick_kernel(int64_t T, int K, int N, bool glu) {
   const double slabs = double((K + 127) / 128), mats = glu ? 2.0 : 1.0;
@@ -844,7 +845,7 @@ static I8Kernel pick_kernel(int64_t T, int K, int N, bool glu) {
     return std::ceil(double((T + bm - 1) / bm) * double((N + oc - 1) / oc) / 256.0);
   };
   const double c32 = per_cu(32, 64), c64 = per_cu(64, 64), c128 = per_cu(128, 128);
-  double least = std::max(slabs * c32 * (c32 == 1.0 ? 0.16 : 0.19) + 2.85, mb * 0.14 + 3.2);
+  double least = std::max(slabs * c32 * (c32 == 1.0 ? 0.16 : 0.19) + 2.85 + 0.5 * (c32 - 1.0), mb * 0.14 + 3.2);
   I8Kernel pick = kTile32;
   auto offer = [&](I8Kernel k, double us) {
     if (us < least) {
@@ -853,10 +854,10 @@ static I8Kernel pick_kernel(int64_t T, int K, int N, bool glu) {
     }
   };
   if (per_cu(32, 32) == 1.0) offer(kTile32Narrow, std::max(slabs * 0.145 + 2.85, mb * 0.144 + 3.2));
-  offer(kTile64, std::max(slabs * c64 * 0.26 + 3.3, mb * 0.14 + 3.6));
+  offer(kTile64, std::max(slabs * c64 * 0.26 + 3.3 + 0.3 * (c64 - 1.0), mb * 0.14 + 3.6));
   if (c64 == 1.0) offer(kTile64Deep, std::max(slabs * 0.20 + 3.9, mb * 0.14 + 4.0));
-  offer(kTile128, slabs * (c128 == 1.0 ? 0.56 : c128 * 0.65) + 3.7);
-  offer(kTile256, per_cu(256, 256) * (slabs * 1.6 + 4.0));
+  offer(kTile128, slabs * (c128 == 1.0 ? 0.56 : c128 * 0.65) + 3.7 + 2.0 * (c128 - 1.0));
+  offer(kTile256, per_cu(256, 256) * (slabs * 1.6 + 4.0) + 3.0);
   if (T <= 16 || (T <= 32 && !glu)) {
     const double wgs = (N + 15) / 16, rounds = std::ceil(wgs / 256.0) * 256.0;
     const double stream = 16e-6 * mats * K * (wgs <= 256.0 ? 256.0 : (wgs + rounds) / 2);
