@@ -468,13 +468,16 @@ def alloc_dense_workspace(cfg: DenseConfig, device="cuda") -> torch.Tensor:
 
 def dense_weights_struct(w: dict) -> DenseWeights:
     """Weight struct of a dict of CUDA tensors: w_gate, w_up [I, H] and w_down [H, I] int8,
-    s_gate, s_up [I] and s_down [H] fp32.  It holds pointers only: keep the tensors alive."""
+    s_gate, s_up [I] and s_down [H] fp32.  It holds pointers only: keep the tensors alive.  Its
+    sizes and device stay with it, for dense_residual_i8 to compare."""
     I, H = _rows_of("w_gate", w["w_gate"])
     dev = _device()
     shapes = {"w_gate": (I, H), "w_up": (I, H), "w_down": (H, I), "s_gate": (I,), "s_up": (I,),
               "s_down": (H,)}
-    return DenseWeights(*[_arg(n, w[n], shapes[n], torch.int8 if n[0] == "w" else torch.float32, dev)
-                          for n, _ in DenseWeights._fields_])
+    wst = DenseWeights(*[_arg(n, w[n], shapes[n], torch.int8 if n[0] == "w" else torch.float32, dev)
+                         for n, _ in DenseWeights._fields_])
+    wst.made_for = (H, I, dev)
+    return wst
 
 
 def dense_residual_i8(cfg: DenseConfig, x, norm_weight, wst: DenseWeights, ws,
@@ -492,6 +495,9 @@ def dense_residual_i8(cfg: DenseConfig, x, norm_weight, wst: DenseWeights, ws,
     else:
         op = _arg("x_out", x_out, (T, H), dtype, dev)
     wp = _arg("ws", ws, (ws.numel(),), torch.uint8, dev)
+    if getattr(wst, "made_for", (H, cfg.intermediate, dev)) != (H, cfg.intermediate, dev):
+        raise ValueError(f"wst: made for (hidden, intermediate, device) {wst.made_for}, the call "
+                         f"has {(H, cfg.intermediate, dev)}")
     _check(load_library().moe_dense_residual_i8(ctypes.byref(cfg), xp, gp, eps, ctypes.byref(wst),
                                                 op, wp, ws.numel(), _raw_stream(dev)))
     return x_out

@@ -527,6 +527,25 @@ def test_binding_refuses(moe):
         moe.norm_quant_rows(torch.zeros(4, 64, device="cuda"), "i8", torch.ones(60, device="cuda"))
 
 
+def test_layer_refuses_weights_of_other_sizes(moe):
+    w, gamma = layer(gen(3), 64, 32, "bf16")
+    x = torch.zeros(2, 64, dtype=torch.bfloat16, device="cuda")
+    wst = moe.dense_weights_struct(w)
+    for T, I in ((2, 48), (3, 32)):
+        cfg = moe.make_dense_config(T, 64, I)
+        with pytest.raises(ValueError):
+            moe.dense_residual_i8(cfg, x, gamma, wst, moe.alloc_dense_workspace(cfg))
+    cfg = moe.make_dense_config(2, 64, 32)
+    ws = moe.alloc_dense_workspace(cfg)
+    with pytest.raises(moe.MoeError):
+        moe.dense_residual_i8(cfg, x, gamma, wst, ws[:256])
+    with pytest.raises(ValueError):
+        moe.dense_weights_struct(dict(w, w_up=w["w_up"][:16]))
+    with pytest.raises(ValueError):
+        moe.dense_weights_struct(dict(w, s_down=w["s_gate"]))
+    assert torch.equal(moe.dense_residual_i8(cfg, x, gamma, wst, ws), x)      # zero rows stay zero
+
+
 @pytest.mark.parametrize("T", [4, 300])
 def test_dense_layer_then_moe_block(moe, T):
     """The start of a decoder stack: the dense layer 0, then an MoE block on the same residual
