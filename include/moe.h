@@ -365,7 +365,8 @@ int moe_linear_i8(int64_t rows, int32_t in_width, int32_t out_width, int32_t out
 /*
  * The gated pair of such products and its activation in one kernel:
  *   h[t,n] = round(silu(g) * u),  g = x_scales[t] s_gate[n] sum_k x[t,k] w_gate[n,k],  u likewise.
- * Arguments and limits as moe_linear_i8.
+ * Arguments and limits as moe_linear_i8.  Here the last fp32 bits of silu may differ between
+ * batch sizes, which choose the kernel.
  */
 int moe_glu_i8(int64_t rows, int32_t in_width, int32_t out_width, int32_t out_dtype,
                const int8_t* x, const float* x_scales, const int8_t* w_gate, const float* s_gate,
